@@ -37,6 +37,9 @@ __all__ = [
     "quantize_activations", "nvfp4_blocked_scales_size", "nvfp4_scales_to_blocked",
     "scales_to_blocked",
     "diag_hessian", "global_scale", "scale_sweep_quantize", "dequantize", "quantize_layer",
+    "KVCacheDesc", "KVCache", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_copy_pages",
+    "nvfp4_kv_attention_workspace_size", "nvfp4_kv_attention", "nvfp4_debug_kv_stalls",
+    "kv_append", "kv_read", "kv_copy_pages", "kv_attention",
 ]
 
 STATUS = {0: "NVFP4_OK", -1: "NVFP4_ERR_INVALID_ARG", -2: "NVFP4_ERR_SHAPE",
@@ -96,6 +99,14 @@ class GroupedInput(C.Structure):
                 ("ldx", _i64), ("h", _vp)]
 
 
+class KVCacheDesc(C.Structure):
+    """nvfp4_kv_cache"""
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
+                ("k_S", _vp), ("v_S", _vp), ("num_pages", _i64), ("code_page_stride", _i64),
+                ("scale_page_stride", _i64), ("page_size", _int), ("kv_heads", _int),
+                ("head_dim", _int)]
+
+
 _SIGS = {
     "nvfp4_version": ([], _int),
     "nvfp4_last_cuda_error": ([], _int),
@@ -148,6 +159,15 @@ _SIGS = {
     "nvfp4_global_scale_batched_workspace_size": ([C.POINTER(MatrixDesc), _i64], _sz),
     "nvfp4_global_scale_batched": ([C.POINTER(MatrixDesc), _i64, _f32, _vp, _vp, _vp, _vp, _sz,
                                     _vp], _int),
+    "nvfp4_kv_append": ([C.POINTER(KVCacheDesc), _vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _vp,
+                         _vp, _vp], _int),
+    "nvfp4_kv_read": ([C.POINTER(KVCacheDesc), _vp, _i64, _int, _vp, _vp, _vp], _int),
+    "nvfp4_kv_copy_pages": ([C.POINTER(KVCacheDesc), _i64, _i64, _i64, _vp, _vp, _i64, _vp], _int),
+    "nvfp4_kv_attention_workspace_size": ([_i64, _i64, _i64, _int, _int, _int], _sz),
+    "nvfp4_kv_attention": ([C.POINTER(KVCacheDesc), _vp, _int, _int, _i64, _i64, _i64, _vp, _vp, _vp,
+                            _i64, _i64, _i64, _i64, _f32, _int, _i64, _vp, _i64, _i64, _vp, _vp, _sz,
+                            _vp], _int),
+    "nvfp4_debug_kv_stalls": ([C.POINTER(C.c_uint), _int], _int),
     "nvfp4_scale_sweep_quantize_batched_workspace_size": ([_i64], _sz),
     "nvfp4_scale_sweep_quantize_batched": ([C.POINTER(SweepDesc), _i64, _int, _int, _vp, _sz, _vp],
                                            _int),
@@ -466,6 +486,51 @@ def nvfp4_scale_sweep_quantize_batched(descs, lo, hi, workspace, workspace_bytes
     arr = _desc_array(SweepDesc, descs)
     _check("nvfp4_scale_sweep_quantize_batched", lib().nvfp4_scale_sweep_quantize_batched(
         arr, len(descs), int(lo), int(hi), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_append(cache, K, V, type, tokens, k_token_stride, k_head_stride, v_token_stride,
+                    v_head_stride, slots, status, stream=None):
+    """cache: KVCacheDesc."""
+    _check("nvfp4_kv_append", lib().nvfp4_kv_append(
+        C.byref(cache), _ptr(K), _ptr(V), type, tokens, k_token_stride, k_head_stride,
+        v_token_stride, v_head_stride, _ptr(slots), _ptr(status), _stream(stream)))
+
+
+def nvfp4_kv_read(cache, slots, tokens, type, K, V, stream=None):
+    _check("nvfp4_kv_read", lib().nvfp4_kv_read(
+        C.byref(cache), _ptr(slots), tokens, type, _ptr(K), _ptr(V), _stream(stream)))
+
+
+def nvfp4_kv_copy_pages(cache, layers, code_layer_stride, scale_layer_stride, src, dst, n,
+                        stream=None):
+    """src, dst: int32 CPU tensors."""
+    _check("nvfp4_kv_copy_pages", lib().nvfp4_kv_copy_pages(
+        C.byref(cache), layers, code_layer_stride, scale_layer_stride, _ptr(src), _ptr(dst), n,
+        _stream(stream)))
+
+
+def nvfp4_kv_attention_workspace_size(batch, max_q, max_kv, q_heads, kv_heads, head_dim) -> int:
+    return lib().nvfp4_kv_attention_workspace_size(batch, max_q, max_kv, q_heads, kv_heads,
+                                                   head_dim)
+
+
+def nvfp4_kv_attention(cache, Q, type, q_heads, total_q, q_token_stride, q_head_stride, q_offsets,
+                       kv_lengths, table, table_stride, batch, max_q, max_kv, sm_scale, causal,
+                       window, out, o_token_stride, o_head_stride, lse, workspace, workspace_bytes,
+                       stream=None):
+    _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
+        C.byref(cache), _ptr(Q), type, q_heads, total_q, q_token_stride, q_head_stride,
+        _ptr(q_offsets), _ptr(kv_lengths), _ptr(table), table_stride, batch, max_q, max_kv,
+        float(sm_scale), int(causal), window, _ptr(out), o_token_stride, o_head_stride, _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_debug_kv_stalls(reset: bool = False) -> int:
+    """How many waits inside the K/V cache's kernels were given up (0 in a
+    correct run); for tests."""
+    n = C.c_uint(0)
+    _check("nvfp4_debug_kv_stalls", lib().nvfp4_debug_kv_stalls(C.byref(n), int(bool(reset))))
+    return n.value
 
 
 # -------------------------------------------------------- tensor conveniences
@@ -797,3 +862,222 @@ def scale_sweep_quantize_batched(Ws, hs, Ss, lo: int = -9, hi: int = 6, want_off
     ws = _workspace(nb, Ws[0].device)
     nvfp4_scale_sweep_quantize_batched(descs, lo, hi, ws, ws.numel(), stream)
     return outs
+
+
+# ------------------------------------------------------------------ K/V cache
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class KVCache:
+    """A paged NVFP4 K/V cache (nvfp4_kv_cache) over tensors of the caller:
+    k_codes, v_codes uint8 [pages, kv_heads, page_size, head_dim/2], k_scales,
+    v_scales uint8 [pages, kv_heads, page_size, head_dim/16] and k_S, v_S float32
+    [kv_heads], all CUDA.  Each may have a leading dimension of layers; a cache of
+    several layers serves kv_copy_pages, and layer(i) is one of its layers.
+    Pages (and layers) may have any stride; a page is contiguous."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_S", "v_S", "layers", "device", "desc")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_S, v_S):
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_S, self.v_S = k_S, v_S
+        shape, small = k_codes.shape, k_scales.shape
+        dims = len(shape)
+        if dims not in (4, 5):
+            raise ValueError("codes must be [pages, kv_heads, page_size, head_dim/2], or that after layers")
+        lead, dim = shape[:-1], 2 * shape[-1]
+        if small[:-1] != lead or 16 * small[-1] != dim or v_codes.shape != shape or v_scales.shape != small:
+            raise ValueError("codes and scales of K and V must agree in shape")
+        stride, small_stride = k_codes.stride(), k_scales.stride()
+        if v_codes.stride() != stride or v_scales.stride() != small_stride:
+            raise ValueError("K and V must have the same strides")
+        h, p = shape[-3], shape[-2]
+        if stride[-3:] != (p * dim // 2, dim // 2, 1) or small_stride[-3:] != (p * dim // 16, dim // 16, 1):
+            raise ValueError("a page must be contiguous")
+        self.layers = shape[0] if dims == 5 else 1
+        s_shape = (self.layers, h) if dims == 5 else (h,)
+        self.device = k_codes.device
+        for t, kind in ((k_codes, torch.uint8), (k_scales, torch.uint8), (v_codes, torch.uint8),
+                        (v_scales, torch.uint8), (k_S, torch.float32), (v_S, torch.float32)):
+            if t.dtype != kind or t.device != self.device or not t.is_cuda:
+                raise ValueError("codes and scales must be uint8, S float32, on one CUDA device")
+        if k_S.shape != s_shape or v_S.shape != s_shape or not k_S.is_contiguous() or not v_S.is_contiguous():
+            raise ValueError("S must be contiguous [kv_heads], or [layers, kv_heads]")
+        self.desc = KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), shape[-4],
+                                stride[-4], small_stride[-4], p, h, dim)
+
+    @classmethod
+    def empty(cls, pages, page_size, kv_heads, head_dim, k_S, v_S, layers=None):
+        """A new cache of zeroed pages on the device of k_S."""
+        lead = (pages, kv_heads, page_size) if layers is None else (layers, pages, kv_heads, page_size)
+        a = [torch.zeros(*lead, head_dim // n, dtype=torch.uint8, device=k_S.device) for n in (2, 16, 2, 16)]
+        return cls(*a, k_S, v_S)
+
+    def layer(self, i):
+        if self.k_codes.dim() != 5:
+            raise ValueError("a cache of one layer")
+        return KVCache(self.k_codes[i], self.k_scales[i], self.v_codes[i], self.v_scales[i], self.k_S[i],
+                       self.v_S[i])
+
+    @property
+    def page_size(self):
+        return self.desc.page_size
+
+    @property
+    def kv_heads(self):
+        return self.desc.kv_heads
+
+    @property
+    def head_dim(self):
+        return self.desc.head_dim
+
+
+def _one_layer(cache):
+    if cache.k_codes.dim() != 4:
+        raise ValueError("pass one layer of the cache (cache.layer(i))")
+    return cache.desc
+
+
+def _kv_rows(t, name, heads, dim, device, types):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype not in types or t.device != device:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] on the cache's device, of a supported type")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t
+
+
+def _int_vector(t, name, kind, device, n=None):
+    if t.dtype != kind or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous {kind} vector" + (f" of {n}" if n is not None else "") +
+                         " on the cache's device")
+    return t
+
+
+class _On:
+    """Makes a device current for a call, and a given stream current for what
+    the call allocates (so that the allocator knows where it is used)."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
+              status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantizes rows K, V [tokens, kv_heads, head_dim] (bf16, fp16 or float32; any
+    token and head strides that are multiples of 16 bytes) into the cache at
+    slots (int64 [tokens], page * page_size + row; negative: skipped; the others
+    distinct).  status: int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN."""
+    d = _one_layer(cache)
+    _kv_rows(K, "K", d.kv_heads, d.head_dim, cache.device, _TYPES)
+    _kv_rows(V, "V", d.kv_heads, d.head_dim, cache.device, (K.dtype,))
+    n = K.shape[0]
+    if V.shape[0] != n:
+        raise ValueError("K and V must have as many tokens")
+    _int_vector(slots, "slots", torch.int64, cache.device, n)
+    if status is not None:
+        _int_vector(status, "status", torch.int32, cache.device, 1)
+    with _On(cache.device, stream):
+        nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, K.stride(0), K.stride(1), V.stride(0), V.stride(1),
+                        slots, status)
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, out=None, stream=None):
+    """The rows at slots as numbers: (K, V) [tokens, kv_heads, head_dim] of dtype; 0
+    where a slot is negative.  out: a pair of contiguous tensors to write."""
+    d = _one_layer(cache)
+    _int_vector(slots, "slots", torch.int64, cache.device)
+    if dtype not in _TYPES:
+        raise ValueError("dtype must be bfloat16, float16 or float32")
+    n = slots.numel()
+    with _On(cache.device, stream):
+        if out is None:
+            K, V = (torch.empty(n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device) for _ in range(2))
+        else:
+            K, V = (_kv_rows(t, "out", d.kv_heads, d.head_dim, cache.device, (dtype,)) for t in out)
+            if not (K.is_contiguous() and V.is_contiguous() and K.shape[0] == V.shape[0] == n):
+                raise ValueError("out must be two contiguous tensors with a row for every slot")
+        nvfp4_kv_read(d, slots, n, _TYPES[dtype], K, V)
+    return K, V
+
+
+def kv_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
+    """Page dst[i] becomes page src[i] in every layer of the cache.  src, dst: page
+    ids on the host (int32 CPU tensors or sequences); no page may be written
+    twice, or both read and written."""
+    src, dst = (torch.as_tensor(t, dtype=torch.int32, device="cpu").contiguous() for t in (src, dst))
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be lists of as many pages")
+    many = cache.k_codes.dim() == 5
+    with _On(cache.device, stream):
+        nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
+                            cache.k_scales.stride(0) if many else 0, src, dst, src.numel())
+
+
+def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_lengths: torch.Tensor,
+                 page_table: torch.Tensor, max_q: int, max_kv: int, sm_scale: float | None = None,
+                 causal: bool = True, window: int = 0, want_lse: bool = False, out=None, lse=None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's new tokens, rows q_offsets[b]..q_offsets[b+1] of
+    Q [total, q_heads, head_dim] (bf16 or fp16), over its kv_lengths[b] cached
+    tokens, the new ones included.  q_offsets int32 [batch+1], kv_lengths int32
+    [batch], page_table int32 [batch, pages per sequence]; max_q, max_kv: bounds
+    of the lengths, known to the host.  sm_scale: 1 / sqrt(head_dim) by default.
+    Returns out, or (out, lse) with lse float32 [total, q_heads]."""
+    d = _one_layer(cache)
+    dev = cache.device
+    if Q.dim() != 3:
+        raise ValueError("Q must be [total, q_heads, head_dim]")
+    heads = Q.shape[1]
+    _kv_rows(Q, "Q", heads, d.head_dim, dev, (torch.bfloat16, torch.float16))
+    _int_vector(kv_lengths, "kv_lengths", torch.int32, dev)
+    batch, total = kv_lengths.numel(), Q.shape[0]
+    _int_vector(q_offsets, "q_offsets", torch.int32, dev, batch + 1)
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
+            or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1)
+            or (batch > 1 and page_table.stride(0) < page_table.shape[1])):
+        raise ValueError("page_table must be int32 [batch, pages], rows contiguous, on the cache's device")
+    if max_kv > page_table.shape[1] * d.page_size:
+        raise ValueError("max_kv is more than the page table's rows hold")
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty(total, heads, d.head_dim, dtype=Q.dtype, device=dev)
+        else:
+            _kv_rows(out, "out", heads, d.head_dim, dev, (Q.dtype,))
+            if out.shape[0] != total:
+                raise ValueError("out must have Q's rows")
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (total, heads) or lse.device != dev or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous float32 [total, q_heads]")
+        elif want_lse:
+            lse = torch.empty(total, heads, dtype=torch.float32, device=dev)
+        if batch and total and max_q > 0:
+            nb = nvfp4_kv_attention_workspace_size(batch, max_q, max_kv, heads, d.kv_heads, d.head_dim)
+            if nb == 0:
+                raise NVFP4Error("nvfp4_kv_attention_workspace_size", -1)
+            if workspace is None:
+                workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, Q.stride(0), Q.stride(1), q_offsets,
+                           kv_lengths, page_table, max(page_table.stride(0), page_table.shape[1]),
+                           batch, max_q, max_kv,
+                           d.head_dim ** -0.5 if sm_scale is None else sm_scale, causal, window, out,
+                           out.stride(0), out.stride(1), lse, workspace,
+                           workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return (out, lse) if lse is not None else out

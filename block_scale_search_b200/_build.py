@@ -18,6 +18,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-shared", "-Xcompiler", "-fPIC",
+    "-t", "0",  # the sources are compiled side by side
     # IEEE division/sqrt and denormals stay on (nvcc defaults); no fast-math.
 ]
 

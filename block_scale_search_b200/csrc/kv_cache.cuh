@@ -1,0 +1,61 @@
+// kv_cache.cuh -- the paged NVFP4 key/value cache: launch functions and the
+// helpers that its kernels share.
+//
+// Layout of one tensor (K or V) of one layer: pages of `page` tokens,
+//   codes  [page id][KV head][row][dim / 2]    page stride given in bytes
+//   scales [page id][KV head][row][dim / 16]   page stride given in bytes
+// so that 16 rows of one head are one contiguous piece of 8 * dim code bytes
+// and one of dim scale bytes: what the attention kernels copy at a time.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "nvfp4hs.h"
+
+namespace nvfp4 {
+
+// A row's element type of the calls that take several.
+enum : int { kBf16 = NVFP4_TYPE_BF16, kFp16 = NVFP4_TYPE_FP16, kFp32 = NVFP4_TYPE_FP32 };
+
+struct KvRows {  // strided rows [token][head][dim] of K or V, strides in elements
+  const void* p;
+  int64_t token_stride, head_stride;
+};
+
+// SM count of the current device, cached (0 on failure).
+int sm_count();
+
+cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvRows& V, int type,
+                             int64_t tokens, const int64_t* slots, int* status, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_kv_read(const nvfp4_kv_cache& c, int64_t tokens, const int64_t* slots, int type,
+                           void* K, void* V, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_copy_pages(const nvfp4_kv_cache& c, int64_t layers,
+                                 int64_t code_layer_stride, int64_t scale_layer_stride,
+                                 const int* src, const int* dst, int64_t n, int num_sms,
+                                 cudaStream_t stream);
+
+// One attention call, checked by the entry point.
+struct KvAttention {
+  nvfp4_kv_cache c;
+  const void* Q;
+  int64_t q_token_stride, q_head_stride;
+  void* out;
+  int64_t o_token_stride, o_head_stride;
+  float* lse;  // [total_q][q_heads] or NULL
+  const int* q_offsets;
+  const int* kv_lengths;
+  const int* table;
+  int64_t table_stride;
+  int type, q_heads, batch, total_q, max_q, max_kv, causal, window;
+  float scale;
+};
+
+size_t kv_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
+                                    int kv_heads, int head_dim, int num_sms);
+cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_sms,
+                                cudaStream_t stream);
+
+}  // namespace nvfp4

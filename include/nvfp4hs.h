@@ -588,6 +588,131 @@ int nvfp4_scales_to_blocked(const uint8_t* scales, int64_t rows, int64_t cols, i
 int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* S,
                      int64_t out, int64_t in, float* W_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged K/V cache in NVFP4 (no counterpart on the pages: the format of
+ * H-Scale summary sec. 3 applied to attention's cache, which a W4A4 deployment
+ * keeps beside its weights and activations).
+ *
+ * A cache holds, for K and for V, pages of page_size tokens:
+ *   codes   uint8, page p at p * code_page_stride bytes:
+ *           [kv_heads][page_size][head_dim / 2], contiguous
+ *   scales  uint8, page p at p * scale_page_stride bytes:
+ *           [kv_heads][page_size][head_dim / 16], contiguous
+ *   S       float [kv_heads]
+ * with rows packed as the codes and scales of a weight row are (groups of 16
+ * along head_dim).  A token's slot is page * page_size + its row in the page.
+ *   num_pages   1 .. 2^31 - 1.
+ *   page_size   a power of two, 16 .. 65536.
+ *   head_dim    a multiple of 16 up to 1024 (attention: 64 or 128).
+ *   k_codes, k_scales, v_codes, v_scales and their strides are 16-byte
+ *   aligned; the strides are at least a page's bytes; S is 4-byte aligned.
+ * The struct is read during the call and may be reused at once.
+ * ------------------------------------------------------------------------ */
+typedef struct nvfp4_kv_cache {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    const float* k_S;
+    const float* v_S;
+    int64_t num_pages, code_page_stride, scale_page_stride;
+    int page_size, kv_heads, head_dim;
+} nvfp4_kv_cache;
+
+/* Element types of rows. */
+enum nvfp4_type { NVFP4_TYPE_BF16 = 0, NVFP4_TYPE_FP16 = 1, NVFP4_TYPE_FP32 = 2 };
+
+/* Quantize rows of K and V and write them at their slots.  Per group of 16:
+ * the scale is the base code of nvfp4_scale_sweep_quantize (fl32(fl32(a / 6) /
+ * S) rounded to E4M3, at least code 1; 0 for a zero group), without a search,
+ * and each code is the exact round-to-nearest-even decision.  Values past 6 *
+ * 448 * S saturate.  A group that holds Inf or NaN gets scale byte 0x7F (NaN)
+ * and zero codes, so that whatever attends to it sees NaN.
+ *   K, V       [tokens][kv_heads][head_dim] of `type`, strides in elements;
+ *              16-byte aligned, strides multiples of 16 bytes.
+ *   slots      DEVICE int64 [tokens], 8-byte aligned.  A token whose slot is
+ *              negative (padding) or not in the cache is skipped.  The other
+ *              slots must be distinct: of tokens that share one, each group
+ *              may come from any of them.
+ *   status     int, device scalar, may be NULL: the call first sets it to
+ *              NVFP4_OK (an asynchronous memset); NVFP4_ERR_NONFINITE when a
+ *              written group held Inf or NaN.
+ * Rows of the cache that no slot names are left as they were. */
+int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* K, const void* V, int type,
+                    int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                    int* status, void* stream);
+
+/* Read rows back: K[t], V[t] = fl32(code * scale) * S of slot slots[t], rounded
+ * once more to `type` where that has 16 bits; 0 where the slot is negative or
+ * not in the cache.
+ *   K, V       [tokens][kv_heads][head_dim] of `type`, contiguous, 32-byte
+ *              aligned (written). */
+int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tokens, int type,
+                  void* K, void* V, void* stream);
+
+/* Copy pages: page dst[i] becomes page src[i], K and V, codes and scales, in
+ * every layer.  What forking a sequence (its last, partly filled page) and
+ * compacting a cache need; the page tables are the caller's to change.
+ *   layers     caches of the same shape whose pointers follow those of `cache`
+ *              at code_layer_stride and scale_layer_stride bytes (multiples of
+ *              16; ignored for one layer); 0 .. 65535.
+ *   src, dst   HOST arrays of n page ids, read before the call returns (they
+ *              travel in the launches' parameters, so a captured call replays
+ *              the pages it was captured with).
+ * A page id outside [0, num_pages), a page that is written twice, or one that
+ * is both read and written returns NVFP4_ERR_INVALID_ARG with nothing
+ * enqueued. */
+int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t code_layer_stride,
+                        int64_t scale_layer_stride, const int32_t* src, const int32_t* dst,
+                        int64_t n, void* stream);
+
+/* Attention of each sequence's new tokens over its cached ones (which include
+ * the new: append them first).  Sequence b has Lq = q_offsets[b+1] -
+ * q_offsets[b] query tokens, rows q_offsets[b].. of Q, and Lk = kv_lengths[b]
+ * cached tokens, token j in page table[b * table_stride + j / page_size].
+ * Query i stands at position p = Lk - Lq + i and sees the tokens j < Lk with
+ * j <= p (causal) and j > p - window (window > 0).  Head q reads KV head
+ * q / (q_heads / kv_heads).
+ *   out = softmax(sm_scale * q . K) V;  lse = log of the sum of the
+ *   exponentials (natural).  A row that sees no token: out 0, lse -inf.
+ * A page id outside [0, num_pages) hides its tokens.  Cached values behind Lk
+ * and in hidden places are never used, whatever they hold.  Rows of Q that
+ * hold Inf or NaN give NaN.  Rows of out and lse that belong to no sequence are
+ * left as they were.
+ *   Q, out     [total_q][q_heads][head_dim] of `type` (BF16 or FP16), strides in
+ *              elements; 16-byte aligned, strides multiples of 16 bytes.  out
+ *              must not overlap Q.
+ *   lse        float [total_q][q_heads] or NULL, 4-byte aligned.
+ *   q_offsets  DEVICE int32 [batch + 1], non-decreasing; kv_lengths DEVICE
+ *              int32 [batch]; table DEVICE int32.  Read on the device: values
+ *              out of range are clamped and never lead outside the buffers.
+ *   max_q, max_kv  host bounds of Lq and Lk (longer ones are cut to them),
+ *              0 <= max_kv <= table_stride * page_size; a captured call serves
+ *              any lengths within them.
+ *   causal     0 or 1; window >= 0, 0 for none; a window needs causal.
+ *   batch      0 .. 65535; total_q, max_q < 2^31; q_heads a multiple of
+ *              kv_heads, at most 1024.
+ *   workspace  nvfp4_kv_attention_workspace_size() bytes (device dependent; 0
+ *              for invalid arguments or no device), 256-byte aligned; needs no
+ *              initialisation.  Calls that may overlap need one each.
+ * FP32 sums and softmax statistics; the probabilities are rounded to FP16 for
+ * the tensor cores.  The result depends on the lengths, the bounds and the
+ * number of SMs, not on timing. */
+size_t nvfp4_kv_attention_workspace_size(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
+                                         int kv_heads, int head_dim);
+int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* Q, int type, int q_heads,
+                       int64_t total_q, int64_t q_token_stride, int64_t q_head_stride,
+                       const int32_t* q_offsets, const int32_t* kv_lengths, const int32_t* table,
+                       int64_t table_stride, int64_t batch, int64_t max_q, int64_t max_kv,
+                       float sm_scale, int causal, int64_t window, void* out,
+                       int64_t o_token_stride, int64_t o_head_stride, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Test support: how often a wait inside the attention kernels was given up
+ * (they are bounded; never in a correct run).  Synchronises with the device. */
+int nvfp4_debug_kv_stalls(unsigned int* count, int reset);
+
 #ifdef __cplusplus
 }
 #endif
