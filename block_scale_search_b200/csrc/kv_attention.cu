@@ -27,7 +27,7 @@
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
 //
-// Work split: the tiles (16 tokens) of all (sequence, row block, KV head)
+// Work split: the tiles (32 tokens) of all (sequence, row block, KV head)
 // items form one line; each CTA takes an equal piece of it, cutting items
 // where it must, so ragged batches and single long sequences fill the GPU
 // alike.  A CTA's warps take tiles in turn, each with its own ring of bulk
@@ -45,9 +45,25 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;    // tokens
-constexpr int kStages = 4;   // tiles in flight per warp
+constexpr int kTile = 32;    // tokens a warp takes at a time, in two halves of 16
+constexpr int kHalf = kTile / 2;
+constexpr int kStages = 2;   // tiles of a warp's ring
+// What starting and finishing an item costs a CTA, in tiles: its page ids and
+// queries arrive in two trips to memory, its warps meet twice at the end.
+constexpr int kItemCost = 8;
 constexpr float kSlack = 8.0f;  // log2 by which a score may pass the running maximum
+
+// Resident CTAs the kernel is built for (its registers and shared memory).
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : (nt == 2 ? 4 : 2); }
+
+// Shared memory: the rings [warp][stage] and the queries' operands [warp][8-row
+// tile][word][lane] of 16 bytes; once an item's tiles are used up, the join
+// area, sums [warp][R][D] and maxima and sums [warp][R][2], lies over both.
+__host__ __device__ constexpr int ring_bytes(int D) { return kWarps * kStages * 2 * kTile * (D / 2 + D / 16); }
+__host__ __device__ constexpr int rows_smem(int D, int NT) {
+  const int use = ring_bytes(D) + kWarps * NT * (D / 32) * 512, join = kWarps * 8 * NT * (D + 2) * 4;
+  return use > join ? use : join;
+}
 
 struct Params {
   KvAttention a;
@@ -58,39 +74,34 @@ struct Params {
   int ctas;
 };
 
-__device__ unsigned int g_stalls;  // waits given up (never, unless a copy is lost)
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+// 16 bytes to shared memory, or 16 zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done = 0;
-  for (int i = 0; i < (1 << 22); ++i) {
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    if (done) return;
-  }
-  atomicAdd(&g_stalls, 1u);
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
+}
+// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
+// low half of r[i].
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&r)[4]) {
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -127,6 +138,7 @@ __device__ __forceinline__ float to_f32(uint16_t v, int type) {
 struct Seq {
   int q0, lq, lk;     // first query row, new tokens, cached tokens
   int t0, tiles;      // first tile that a query sees, tiles per item (at least 1)
+  int span;           // units of an item on the line of work: kItemCost, then its tiles
   int blocks;         // row blocks
 };
 
@@ -140,14 +152,15 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
   const int first = p.a.window > 0 ? max(0, s.lk - s.lq - p.a.window + 1) : 0;
   s.t0 = first / kTile;
   s.tiles = max(1, (s.lk + kTile - 1) / kTile - s.t0);
+  s.span = s.tiles + kItemCost;
   s.blocks = (s.lq * p.group + R - 1) / R;
   return s;
 }
 
 template <int R>
-__device__ __forceinline__ long long seq_tiles(const Params& p, int b) {
+__device__ __forceinline__ long long seq_units(const Params& p, int b) {
   const Seq s = sequence<R>(p, b);
-  return static_cast<long long>(s.blocks) * p.a.c.kv_heads * s.tiles;
+  return static_cast<long long>(s.blocks) * p.a.c.kv_heads * s.span;
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -156,11 +169,11 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// Sum of seq_tiles over b < n, by the whole CTA (every thread gets it).
+// Sum of seq_units over b < n, by the whole CTA (every thread gets it).
 template <int R>
-__device__ __forceinline__ long long tiles_before(const Params& p, int n, long long* red) {
+__device__ __forceinline__ long long units_before(const Params& p, int n, long long* red) {
   long long v = 0;
-  for (int b = threadIdx.x; b < n; b += kThreads) v += seq_tiles<R>(p, b);
+  for (int b = threadIdx.x; b < n; b += kThreads) v += seq_units<R>(p, b);
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -171,10 +184,10 @@ __device__ __forceinline__ long long tiles_before(const Params& p, int n, long l
   return v;
 }
 
-// Tiles per CTA: an equal share, but no less than two tiles a warp.
-__device__ __forceinline__ long long tiles_per_cta(long long total, int ctas) {
+// Units per CTA: an equal share, but no less than an item of a tile a warp.
+__device__ __forceinline__ long long units_per_cta(long long total, int ctas) {
   const long long share = (total + ctas - 1) / ctas;
-  return share > 2 * kWarps ? share : 2 * kWarps;
+  return share > kWarps + kItemCost ? share : kWarps + kItemCost;
 }
 
 // A row r of a block of a sequence: query r / G, head h G + r % G.
@@ -212,40 +225,34 @@ __device__ __forceinline__ void write_lse(const Params& p, const Seq& s, int h, 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 kv_rows_kernel(const __grid_constant__ Params p) {
   constexpr int R = 8 * NT;
   constexpr int KW = D / 32;            // K words (8 values) per lane and row
   constexpr int VW = D / 64;            // V words per lane and token
-  constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
-  constexpr int kStageBytes = 2 * (kCodes + kScales);
+  constexpr int kCodes = kHalf * D / 2, kScales = kHalf * D / 16;  // of one half, K or V
+  constexpr int kHalfBytes = 2 * (kCodes + kScales);
+  constexpr int kStageBytes = 2 * kHalfBytes;
   extern __shared__ __align__(128) uint8_t smem[];
-  // [warp][stage] tiles, then the join area [warp][R][D] and its maxima and
-  // sums [warp][R][2], then the barriers
-  float* const join_o = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+  float* const join_o = reinterpret_cast<float*>(smem);
   float* const join_ml = join_o + kWarps * R * D;
-  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ long long red[kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, l4 = lane & 3;
   const nvfp4_kv_cache& c = p.a.c;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
-  const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp][0]);
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) mbar_init(bar_u + 8 * s, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
+  constexpr int kRing = ring_bytes(D);
+  uint4* const q = reinterpret_cast<uint4*>(smem + kRing) + warp * NT * KW * 32 + lane;
+  const uint32_t ring_u = smem_u32(ring);
 
-  // this CTA's piece of the line of tiles
-  const long long total = tiles_before<R>(p, p.a.batch, red);
-  const long long per = tiles_per_cta(total, p.ctas);
+  // this CTA's piece of the line of work
+  const long long total = units_before<R>(p, p.a.batch, red);
+  const long long per = units_per_cta(total, p.ctas);
   long long cur = per * blockIdx.x;
   const long long end = min(total, cur + per);
   if (cur >= end) return;
-  // the sequence that holds tile `cur`
+  // the sequence that holds unit `cur`
   int b = 0;
   long long base = 0;
   {
@@ -253,7 +260,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     for (;; b += 32) {
       if (b >= p.a.batch) return;
       const int bb = b + lane;
-      const long long n = bb < p.a.batch ? seq_tiles<R>(p, bb) : 0;
+      const long long n = bb < p.a.batch ? seq_units<R>(p, bb) : 0;
       long long inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -271,72 +278,96 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     }
   }
 
-  uint32_t fill = 0, use = 0;  // tiles this warp has requested and consumed, over all items
   while (cur < end) {
     const Seq s = sequence<R>(p, b);
     const long long in_seq = cur - base;
-    const int item = static_cast<int>(in_seq / s.tiles);
-    const int ts = static_cast<int>(in_seq - static_cast<long long>(item) * s.tiles);
+    const int item = static_cast<int>(in_seq / s.span);
+    const int us = static_cast<int>(in_seq - static_cast<long long>(item) * s.span);
+    const int ue = static_cast<int>(min(static_cast<long long>(s.span), us + (end - cur)));
+    const int ts = max(0, us - kItemCost), te = max(0, ue - kItemCost);  // this CTA's tiles of the item
     const int h = item % c.kv_heads, r0 = item / c.kv_heads * R;
-    const int te = static_cast<int>(min(static_cast<long long>(s.tiles), ts + (end - cur)));
+    auto next_item = [&]() {  // false at the end of the batch
+      cur += ue - us;
+      if (cur >= end) return true;
+      long long n = seq_units<R>(p, b);
+      while (cur >= base + n) {  // also steps over sequences without new tokens
+        base += n;
+        if (++b >= p.a.batch) return false;
+        n = seq_units<R>(p, b);
+      }
+      return true;
+    };
+    if (ts >= te) {  // the piece ends before the item's first tile
+      if (!next_item()) return;
+      continue;
+    }
     const int mine = te - ts > warp ? (te - ts - warp + kWarps - 1) / kWarps : 0;
 
     // ---- bulk copies of this warp's k-th tile of the item
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2);
     const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16);
     const int* const row_table = p.a.table + b * p.a.table_stride;
-    auto page_at = [&](int k) {  // page id of tile k, or -1
-      const int tok = (s.t0 + ts + warp + k * kWarps) * kTile;
+    auto page_at = [&](int k, int half) {  // page id of half a tile, or -1
+      const int tok = (s.t0 + ts + warp + k * kWarps) * kTile + half * kHalf;
       if (k >= mine || tok >= s.lk) return -1;
       const int id = row_table[tok >> p.page_shift];
       return id >= 0 && id < c.num_pages ? id : -1;
     };
-    int ids = page_at(lane), ids_base = 0;  // lane i: page of tile ids_base + i
-    uint32_t live_mask = 0;                 // bit (tile % 32): the tile's page exists
+    // lane i: pages of tile ids_base + i
+    int ids0 = page_at(lane, 0), ids1 = page_at(lane, 1), ids_base = 0;
+    uint32_t dead = 0;  // bits 2 (tile % 16), + 1: no page there (zeros are written)
     int requested = 0;
+    // scale bytes: lanes 8 i .. 8 i + 7 (D = 64: 4 i .. 4 i + 3) copy those of
+    // K (i < 2) or V of half i % 2
+    constexpr int kScaleLanes = kScales / 16;
+    const int sc_part = lane / kScaleLanes;
+    const uint8_t* const sc_src = (sc_part & 2 ? c.v_scales : c.k_scales) + head_scales + lane % kScaleLanes * 16;
+    const uint32_t sc_dst = ring_u + (sc_part & 1) * kHalfBytes + (sc_part & 2 ? kCodes + kScales : 0) + kCodes +
+                            lane % kScaleLanes * 16;
+    const uint8_t* const k_src = c.k_codes + head_codes + lane * 16;
+    const uint8_t* const v_src = c.v_codes + head_codes + lane * 16;
+    const uint32_t code_dst = ring_u + lane * 16;
+    int fill = 0;  // ring position of the next request, in bytes
     auto request = [&]() {
-      if (requested >= mine) return;
-      if (requested == ids_base + 32) {
-        ids_base += 32;
-        ids = page_at(ids_base + lane);
-      }
-      const int id = __shfl_sync(0xFFFFFFFFu, ids, requested - ids_base);
-      const uint32_t st = fill % kStages;
-      const uint32_t bit = 1u << (requested & 31);
-      if (id >= 0) {
-        live_mask |= bit;
-        if (lane == 0) mbar_expect(bar_u + 8 * st, kStageBytes);
-        __syncwarp();
-        if (lane < 4) {
-          const int row = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
-          const bool isv = lane & 2;
-          const uint8_t* src;
-          uint32_t dst = ring_u + st * kStageBytes + (isv ? kCodes + kScales : 0);
-          uint32_t bytes;
-          if (lane & 1) {
-            src = (isv ? c.v_scales : c.k_scales) + id * c.scale_page_stride + head_scales + row * (D / 16);
-            dst += kCodes;
-            bytes = kScales;
-          } else {
-            src = (isv ? c.v_codes : c.k_codes) + id * c.code_page_stride + head_codes + row * (D / 2);
-            bytes = kCodes;
-          }
-          bulk_load(dst, src, bytes, bar_u + 8 * st);
+      if (requested < mine) {
+        if (requested == ids_base + 32) {
+          ids_base += 32;
+          ids0 = page_at(ids_base + lane, 0);
+          ids1 = page_at(ids_base + lane, 1);
         }
-      } else {
-        live_mask &= ~bit;
-        if (lane == 0)  // nothing to copy: complete the phase
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_u + 8 * st) : "memory");
+        const int id0 = __shfl_sync(0xFFFFFFFFu, ids0, requested - ids_base);
+        const int id1 = __shfl_sync(0xFFFFFFFFu, ids1, requested - ids_base);
+        const uint32_t none = (id0 < 0 ? 1u : 0u) | (id1 < 0 ? 2u : 0u);
+        const int sh = 2 * (requested & 15);
+        dead = (dead & ~(3u << sh)) | (none << sh);
+        const int row = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int id = half ? id1 : id0;
+          const int r = half ? (row + kHalf) & (c.page_size - 1) : row;
+          const int64_t off = id < 0 ? 0 : id * c.code_page_stride + r * (D / 2);
+          const int n = id < 0 ? 0 : 16;
+#pragma unroll
+          for (int i = 0; i < kCodes / 512; ++i) {
+            copy16(code_dst + fill + half * kHalfBytes + i * 512, k_src + off + i * 512, n);
+            copy16(code_dst + fill + half * kHalfBytes + kCodes + kScales + i * 512, v_src + off + i * 512, n);
+          }
+        }
+        if (sc_part < 4) {
+          const int id = sc_part & 1 ? id1 : id0;
+          const int r = sc_part & 1 ? (row + kHalf) & (c.page_size - 1) : row;
+          copy16(sc_dst + fill, sc_src + (id < 0 ? 0 : id * c.scale_page_stride + r * (D / 16)), id < 0 ? 0 : 16);
+        }
+        ++requested;
+        fill = fill == (kStages - 1) * kStageBytes ? 0 : fill + kStageBytes;
       }
-      ++requested;
-      ++fill;
+      copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) request();
 
     // ---- query rows: lane (g, l4) holds d [l4 D/4, (l4+1) D/4) of row g of
     // every 8-row tile, in FP16 after scaling the row's maximum to [1, 2)
-    uint32_t q[NT][KW * 4];
     float f[NT][2];              // factor of the scores of columns 2 l4, 2 l4 + 1
     int vlo[NT][2], vhi[NT][2];  // visible tokens of those columns
     int all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row sees
@@ -371,10 +402,18 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       // power of two at or below the maximum, kept where its reciprocal is a
       // normal number; Inf and NaN stay what they are in FP16
       const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-      const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+      float shrink = __uint_as_float((254u - e) << 23);
+      float fs = __uint_as_float(e << 23) * p.scale_log2 * c.k_S[h];
+      // the factor is kept above 0 (a negative one turns Q's sign), so that
+      // it keeps the order of scores and a hidden score's -inf
+      if (fs < 0.0f) fs = -fs, shrink = -shrink;
+      if (fs < 0x1p-120f) fs = 0x1p-120f;
 #pragma unroll
-      for (int i = 0; i < KW * 4; ++i) q[n][i] = pack_f16x2(y[2 * i] * down, y[2 * i + 1] * down);
-      const float fs = up * p.scale_log2 * c.k_S[h];
+      for (int w = 0; w < KW; ++w)
+        q[(n * KW + w) * 32] = make_uint4(pack_f16x2(y[8 * w] * shrink, y[8 * w + 1] * shrink),
+                                          pack_f16x2(y[8 * w + 2] * shrink, y[8 * w + 3] * shrink),
+                                          pack_f16x2(y[8 * w + 4] * shrink, y[8 * w + 5] * shrink),
+                                          pack_f16x2(y[8 * w + 6] * shrink, y[8 * w + 7] * shrink));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         f[n][k] = __shfl_sync(0xFFFFFFFFu, fs, (2 * l4 + k) * 4);
@@ -392,107 +431,128 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     }
 
     float o[NT][VW * 4][4] = {};
-    float m[NT][2], l[NT][2];
+    // running maximum (base-2 exponent), what to add to a score for it (0 while
+    // nothing was seen), and this lane's share of the sum
+    float m[NT][2], down[NT][2] = {}, l[NT][2] = {};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY;
 
     // S^T row r holds token r ^ (r >> 1 & 1): neighbouring rows and the
     // tokens of one V load then differ in parity, which halves the bank
     // conflicts of 64-byte rows
     auto tok = [](int r) { return r ^ ((r >> 1) & 1); };
 
+    int use = 0;  // ring position of the tile in use, in bytes
     for (int k = 0; k < mine; ++k) {
       request();
-      const uint32_t st = use % kStages;
-      mbar_wait(bar_u + 8 * st, (use / kStages) & 1);
-      ++use;
-      const uint8_t* const kc = ring + st * kStageBytes;
-      const uint8_t* const ks = kc + kCodes;
-      const uint8_t* const vc = ks + kScales;
-      const uint8_t* const vs = vc + kCodes;
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* const stage = ring + use;
+      use = use == (kStages - 1) * kStageBytes ? 0 : use + kStageBytes;
       const int tb = (s.t0 + ts + warp + k * kWarps) * kTile;  // first token
-      const bool live = (live_mask >> (k & 31)) & 1;
-      if (live) {
-        // ---- S^T
-        float x[NT][4] = {};
-        uint32_t kw[2][KW];
-        uint32_t ksc[2];  // two scales (D = 64: one, twice)
+      const uint32_t none = (dead >> (2 * (k & 15))) & 3u;
+      const bool edge = tb < all_lo || tb + kTile > all_hi || none != 0;
+      // ---- S^T
+      float x[NT][2][4] = {};
+      uint32_t kw[2][2][KW];
+      uint32_t ksc[2][2];  // two scales (D = 64: one, and a zero)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint8_t* const kc = stage + half * kHalfBytes;
+        const uint8_t* const ks = kc + kCodes;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int t = tok(g) + 8 * j;
+          uint32_t(&k4)[KW] = kw[half][j];
           if constexpr (D == 128) {
             const uint4 v = *reinterpret_cast<const uint4*>(kc + t * 64 + l4 * 16);
-            kw[j][0] = v.x, kw[j][1] = v.y, kw[j][2] = v.z, kw[j][3] = v.w;
-            ksc[j] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + t * 8 + l4 * 2));
+            k4[0] = v.x, k4[1] = v.y, k4[2] = v.z, k4[3] = v.w;
+            ksc[half][j] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + t * 8 + l4 * 2));
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(kc + t * 32 + l4 * 8);
-            kw[j][0] = v.x, kw[j][1] = v.y;
-            ksc[j] = e4m3x2_to_f16x2(ks[t * 4 + l4]);
+            k4[0] = v.x, k4[1] = v.y;
+            ksc[half][j] = e4m3x2_to_f16x2(ks[t * 4 + l4]);
           }
         }
+      }
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          // block of word w: two words a block
-          const uint32_t sel = w < 2 ? 0x1010 : 0x3232;
-          const uint32_t s0 = __byte_perm(ksc[0], 0, sel), s1 = __byte_perm(ksc[1], 0, sel);
+      for (int w = 0; w < KW; ++w) {
+        uint4 qw[NT];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t a[4];
-            a[0] = mul_f16x2(e2m1x2_to_f16x2((kw[0][w] >> (16 * j)) & 0xFFu), s0);
-            a[1] = mul_f16x2(e2m1x2_to_f16x2((kw[1][w] >> (16 * j)) & 0xFFu), s1);
-            a[2] = mul_f16x2(e2m1x2_to_f16x2((kw[0][w] >> (16 * j + 8)) & 0xFFu), s0);
-            a[3] = mul_f16x2(e2m1x2_to_f16x2((kw[1][w] >> (16 * j + 8)) & 0xFFu), s1);
+        for (int n = 0; n < NT; ++n) qw[n] = q[(n * KW + w) * 32];
+        const uint32_t sel = w < 2 ? 0x1010 : 0x3232;  // block of word w: two words a block
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma(x[n], a, q[n][4 * w + 2 * j], q[n][4 * w + 2 * j + 1]);
-          }
-        }
-        const bool edge = tb < all_lo || tb + kTile > all_hi;
-        bool over = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = x[n][i] * f[n][i & 1];
-            if (edge) {
-              const int t = tb + tok(g) + (i & 2) * 4;
-              if (t < vlo[n][i & 1] || t >= vhi[n][i & 1]) y = -INFINITY;
-            }
-            x[n][i] = y;
-            over |= y > m[n][i & 1] + kSlack;
-          }
-        }
-        if (__any_sync(0xFFFFFFFFu, over)) {
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t s0 = __byte_perm(ksc[half][0], 0, sel), s1 = __byte_perm(ksc[half][1], 0, sel);
+          uint32_t e0[4], e1[4];
+          decode_word(kw[half][0][w], e0);
+          decode_word(kw[half][1][w], e1);
+          const uint32_t a[4] = {mul_f16x2(e0[0], s0), mul_f16x2(e1[0], s1), mul_f16x2(e0[1], s0), mul_f16x2(e1[1], s1)};
+          const uint32_t b[4] = {mul_f16x2(e0[2], s0), mul_f16x2(e1[2], s1), mul_f16x2(e0[3], s0), mul_f16x2(e1[3], s1)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float t = fmaxf(x[n][i], x[n][i + 2]);
-              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-              t = fmaxf(t, m[n][i]);
-              const float r = t == m[n][i] ? 1.0f : exp2_approx(m[n][i] - t);
-              m[n][i] = t;
-              l[n][i] *= r;
-#pragma unroll
-              for (int u = 0; u < VW * 4; ++u) o[n][u][i] *= r, o[n][u][i + 2] *= r;
-            }
+            mma(x[n][half], a, qw[n].x, qw[n].y);
+            mma(x[n][half], b, qw[n].z, qw[n].w);
           }
         }
-        uint32_t pb[NT][2];
+      }
+      if (edge) {
+        __syncwarp();  // keeps this a branch
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int t = tb + (i >> 2) * kHalf + tok(g) + (i & 2) * 4;
+            if (t < vlo[n][i & 1] || t >= vhi[n][i & 1] || ((none >> (i >> 2)) & 1)) x[n][i >> 2][i & 3] = -INFINITY;
+          }
+      }
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          over |= fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])) * f[n][i] >
+                  m[n][i] + kSlack;
+      }
+      if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mm = m[n][i & 1];
-            x[n][i] = exp2_approx(x[n][i] - (mm == -INFINITY ? 0.0f : mm));
-            l[n][i & 1] += x[n][i];
+          for (int i = 0; i < 2; ++i) {
+            float t = fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])) * f[n][i];
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+            t = fmaxf(t, m[n][i]);
+            const float r = t == m[n][i] ? 1.0f : exp2_approx(m[n][i] - t);
+            m[n][i] = t;
+            down[n][i] = t == -INFINITY ? 0.0f : -t;
+            l[n][i] *= r;
+#pragma unroll
+            for (int u = 0; u < VW * 4; ++u) o[n][u][i] *= r, o[n][u][i + 2] *= r;
           }
-          pb[n][0] = transpose8x8(pack_f16x2(x[n][0], x[n][1]));
-          pb[n][1] = transpose8x8(pack_f16x2(x[n][2], x[n][3]));
         }
-        // ---- O^T: tokens of the k index 2 l4, 2 l4 + 1, 2 l4 + 8, 2 l4 + 9
-        const int ta = tok(2 * l4), tc = tok(2 * l4 + 1);
+      }
+      uint32_t pb[NT][2][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[n][half][i] = exp2_approx(fmaf(x[n][half][i], f[n][i & 1], down[n][i & 1]));
+          l[n][0] += x[n][half][0] + x[n][half][2];
+          l[n][1] += x[n][half][1] + x[n][half][3];
+          pb[n][half][0] = transpose8x8(pack_f16x2(x[n][half][0], x[n][half][1]));
+          pb[n][half][1] = transpose8x8(pack_f16x2(x[n][half][2], x[n][half][3]));
+        }
+      }
+      // ---- O^T: tokens of the k index 2 l4, 2 l4 + 1, 2 l4 + 8, 2 l4 + 9
+      const int ta = tok(2 * l4), tc = tok(2 * l4 + 1);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint8_t* const vc = stage + half * kHalfBytes + kCodes + kScales;
+        const uint8_t* const vs = vc + kCodes;
         uint32_t vw[4][VW], vsc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -506,15 +566,17 @@ kv_rows_kernel(const __grid_constant__ Params p) {
             vsc[j] = vs[t * 4 + (g >> 1)];
           }
         }
-        uint32_t nan_tokens = 0;  // bit j: vsc[j] is NaN and its token is hidden from some row
+        uint32_t nan_tokens = 0;  // bit j: vsc[j] is NaN and its token may be hidden from some row
         if (edge) {
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int t = tb + (j & 1 ? tc : ta) + (j & 2) * 4;
-            if ((vsc[j] & 0x7Fu) == 0x7Fu) {
+            const int t = tb + half * kHalf + (j & 1 ? tc : ta) + (j & 2) * 4;
+            const bool gone = t >= s.lk || ((none >> half) & 1);
+            if (gone || (vsc[j] & 0x7Fu) == 0x7Fu) {
               // 0 * NaN would reach rows that do not see the token: take it
               // out of the product and give it to the rows that do (below)
-              if (t < s.lk) nan_tokens |= 1u << j;
+              if (!gone) nan_tokens |= 1u << j;
               vsc[j] = 0;
             }
           }
@@ -524,30 +586,28 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           constexpr uint32_t kLow = 0x0F0F0F0Fu;
-          const uint32_t lo_ab = (vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow);
-          const uint32_t hi_ab = ((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow);
-          const uint32_t lo_cd = (vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow);
-          const uint32_t hi_cd = ((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow);
+          uint32_t lo_ab[4], hi_ab[4], lo_cd[4], hi_cd[4];
+          decode_word((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), lo_ab);
+          decode_word(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), hi_ab);
+          decode_word((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), lo_cd);
+          decode_word(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), hi_cd);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            uint32_t a[4];
-            a[0] = mul_f16x2(e2m1x2_to_f16x2((lo_ab >> (8 * u)) & 0xFFu), sab);
-            a[1] = mul_f16x2(e2m1x2_to_f16x2((hi_ab >> (8 * u)) & 0xFFu), sab);
-            a[2] = mul_f16x2(e2m1x2_to_f16x2((lo_cd >> (8 * u)) & 0xFFu), scd);
-            a[3] = mul_f16x2(e2m1x2_to_f16x2((hi_cd >> (8 * u)) & 0xFFu), scd);
+            const uint32_t a[4] = {mul_f16x2(lo_ab[u], sab), mul_f16x2(hi_ab[u], sab),
+                                   mul_f16x2(lo_cd[u], scd), mul_f16x2(hi_cd[u], scd)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma(o[n][4 * w + u], a, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n) mma(o[n][4 * w + u], a, pb[n][half][0], pb[n][half][1]);
           }
         }
         if (edge && __any_sync(0xFFFFFFFFu, nan_tokens != 0)) {
           // the NaN tokens of lane g's own elements, gathered over l4
-#pragma unroll
+#pragma unroll 1
           for (int src = 0; src < 4; ++src) {
             const uint32_t bits = __shfl_sync(0xFFFFFFFFu, nan_tokens, (lane & ~3) | src);
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
               if (!((bits >> j) & 1)) continue;
-              const int t = tb + tok(2 * src + (j & 1)) + (j & 2) * 4;
+              const int t = tb + half * kHalf + tok(2 * src + (j & 1)) + (j & 2) * 4;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -564,7 +624,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       __syncwarp();  // the stage may be written again
     }
 
-    // ---- join the warps
+    // ---- join the warps (their areas lie over all rings)
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -616,16 +677,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     }
     __syncthreads();
 
-    // ---- next item
-    cur += te - ts;
-    if (cur < end) {
-      long long n = seq_tiles<R>(p, b);
-      while (cur >= base + n) {  // also steps over sequences without new tokens
-        base += n;
-        if (++b >= p.a.batch) return;
-        n = seq_tiles<R>(p, b);
-      }
-    }
+    if (!next_item()) return;
   }
 }
 
@@ -640,10 +692,10 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   const int row = blockIdx.x % R, item = blockIdx.x / R;
   const int h = item % p.a.c.kv_heads, rb = item / p.a.c.kv_heads;
   if (rb >= s.blocks || rb * R + row >= s.lq * p.group) return;
-  const long long base = tiles_before<R>(p, b, red);
-  const long long total = tiles_before<R>(p, p.a.batch, red);
-  const long long per = tiles_per_cta(total, p.ctas);
-  const long long first = base + static_cast<long long>(item) * s.tiles, last = first + s.tiles - 1;
+  const long long base = units_before<R>(p, b, red);
+  const long long total = units_before<R>(p, p.a.batch, red);
+  const long long per = units_per_cta(total, p.ctas);
+  const long long first = base + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
   const long long c0 = first / per, c1 = last / per;
   if (c0 == c1) return;
   auto at = [&](long long cta) {
@@ -707,22 +759,19 @@ int row_tiles(int64_t max_q, int q_heads, int kv_heads) {
   return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
 }
 
-int ctas_per_sm(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
-
 int row_ctas(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int nt, int num_sms) {
   const int64_t blocks = (max_q * (q_heads / kv_heads) + 8 * nt - 1) / (8 * nt);
   const double tiles = static_cast<double>(batch) * blocks * kv_heads *
-                       static_cast<double>((max_kv + kTile - 1) / kTile + 1);
+                       static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
   const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(nt);
-  const double want = tiles / (2 * kWarps) + 1.0;
+  const double want = tiles / (kWarps + kItemCost) + 1.0;
   return static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
 }
 
 template <int D, int NT>
 cudaError_t run_rows(Params& p, cudaStream_t stream) {
   constexpr int R = 8 * NT;
-  constexpr int kStageBytes = 2 * kTile * (D / 2 + D / 16);
-  constexpr int smem = kWarps * (kStages * kStageBytes + R * (D + 2) * 4);
+  constexpr int smem = rows_smem(D, NT);
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_rows_kernel<D, NT>),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -763,16 +812,6 @@ cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_s
   if (nt == 1) return run_rows<64, 1>(p, stream);
   if (nt == 2) return run_rows<64, 2>(p, stream);
   return run_rows<64, 4>(p, stream);
-}
-
-unsigned int kv_stalls(bool reset, cudaError_t* e) {
-  unsigned int n = 0;
-  *e = cudaMemcpyFromSymbol(&n, g_stalls, sizeof(n));
-  if (*e == cudaSuccess && reset) {
-    const unsigned int z = 0;
-    *e = cudaMemcpyToSymbol(g_stalls, &z, sizeof(z));
-  }
-  return n;
 }
 
 }  // namespace nvfp4
