@@ -78,8 +78,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 // 16 bytes to shared memory, or 16 zeros where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+template <int kDst, int kSrc>
+__device__ __forceinline__ void copy16(uint32_t dst, uint64_t src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(kDst),
+               "n"(kSrc)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
@@ -238,7 +241,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   float* const join_ml = join_o + kWarps * R * D;
   __shared__ long long red[kWarps];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // from lane 0, so that the compiler takes it, and branches on it, as uniform
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, l4 = lane & 3;
   const nvfp4_kv_cache& c = p.a.c;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
@@ -321,12 +325,16 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     // K (i < 2) or V of half i % 2
     constexpr int kScaleLanes = kScales / 16;
     const int sc_part = lane / kScaleLanes;
-    const uint8_t* const sc_src = (sc_part & 2 ? c.v_scales : c.k_scales) + head_scales + lane % kScaleLanes * 16;
+    const uint64_t sc_src = reinterpret_cast<uint64_t>((sc_part & 2 ? c.v_scales : c.k_scales) + head_scales) +
+                            lane % kScaleLanes * 16;
     const uint32_t sc_dst = ring_u + (sc_part & 1) * kHalfBytes + (sc_part & 2 ? kCodes + kScales : 0) + kCodes +
                             lane % kScaleLanes * 16;
-    const uint8_t* const k_src = c.k_codes + head_codes + lane * 16;
-    const uint8_t* const v_src = c.v_codes + head_codes + lane * 16;
+    const uint64_t k_src = reinterpret_cast<uint64_t>(c.k_codes + head_codes) + lane * 16;
+    const uint64_t v_src = reinterpret_cast<uint64_t>(c.v_codes + head_codes) + lane * 16;
     const uint32_t code_dst = ring_u + lane * 16;
+    // page strides are below 2^32 bytes: one 32 x 32 -> 64 multiply-add
+    const uint32_t code_page = static_cast<uint32_t>(c.code_page_stride);
+    const uint32_t scale_page = static_cast<uint32_t>(c.scale_page_stride);
     int fill = 0;  // ring position of the next request, in bytes
     auto request = [&]() {
       if (requested < mine) {
@@ -340,23 +348,27 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         const uint32_t none = (id0 < 0 ? 1u : 0u) | (id1 < 0 ? 2u : 0u);
         const int sh = 2 * (requested & 15);
         dead = (dead & ~(3u << sh)) | (none << sh);
-        const int row = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int id = half ? id1 : id0;
-          const int r = half ? (row + kHalf) & (c.page_size - 1) : row;
-          const int64_t off = id < 0 ? 0 : id * c.code_page_stride + r * (D / 2);
-          const int n = id < 0 ? 0 : 16;
-#pragma unroll
-          for (int i = 0; i < kCodes / 512; ++i) {
-            copy16(code_dst + fill + half * kHalfBytes + i * 512, k_src + off + i * 512, n);
-            copy16(code_dst + fill + half * kHalfBytes + kCodes + kScales + i * 512, v_src + off + i * 512, n);
-          }
+        const uint32_t row0 = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
+        const uint32_t row1 = (row0 + kHalf) & (c.page_size - 1);
+        const int n0 = id0 < 0 ? 0 : 16, n1 = id1 < 0 ? 0 : 16;
+        const uint32_t p0 = max(id0, 0), p1 = max(id1, 0);
+        const uint64_t off0 = static_cast<uint64_t>(p0) * code_page + row0 * (D / 2);
+        const uint64_t off1 = static_cast<uint64_t>(p1) * code_page + row1 * (D / 2);
+        const uint32_t dst = code_dst + fill;
+        copy16<0, 0>(dst, k_src + off0, n0);
+        copy16<kCodes + kScales, 0>(dst, v_src + off0, n0);
+        copy16<kHalfBytes, 0>(dst, k_src + off1, n1);
+        copy16<kHalfBytes + kCodes + kScales, 0>(dst, v_src + off1, n1);
+        if constexpr (kCodes == 1024) {
+          copy16<512, 512>(dst, k_src + off0, n0);
+          copy16<512 + kCodes + kScales, 512>(dst, v_src + off0, n0);
+          copy16<512 + kHalfBytes, 512>(dst, k_src + off1, n1);
+          copy16<512 + kHalfBytes + kCodes + kScales, 512>(dst, v_src + off1, n1);
         }
-        if (sc_part < 4) {
-          const int id = sc_part & 1 ? id1 : id0;
-          const int r = sc_part & 1 ? (row + kHalf) & (c.page_size - 1) : row;
-          copy16(sc_dst + fill, sc_src + (id < 0 ? 0 : id * c.scale_page_stride + r * (D / 16)), id < 0 ? 0 : 16);
+        if (kScaleLanes == 8 || sc_part < 4) {
+          const bool second = sc_part & 1;
+          const uint64_t off = static_cast<uint64_t>(second ? p1 : p0) * scale_page + (second ? row1 : row0) * (D / 16);
+          copy16<0, 0>(sc_dst + fill, sc_src + off, second ? n1 : n0);
         }
         ++requested;
         fill = fill == (kStages - 1) * kStageBytes ? 0 : fill + kStageBytes;
@@ -429,6 +441,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       all_lo = max(all_lo, __shfl_xor_sync(0xFFFFFFFFu, all_lo, o));
       all_hi = min(all_hi, __shfl_xor_sync(0xFFFFFFFFu, all_hi, o));
     }
+    all_lo = __shfl_sync(0xFFFFFFFFu, all_lo, 0);
+    all_hi = __shfl_sync(0xFFFFFFFFu, all_hi, 0);
 
     float o[NT][VW * 4][4] = {};
     // running maximum (base-2 exponent), what to add to a score for it (0 while

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int64_t kIntMax = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxStride = int64_t{1} << 40;  // guards index arithmetic
+constexpr int64_t kMaxPageStride = (int64_t{1} << 32) - 16;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -33,7 +34,7 @@ int check_cache(const nvfp4_kv_cache* c) {
     return NVFP4_ERR_SHAPE;
   const int64_t rows = static_cast<int64_t>(c->kv_heads) * c->page_size;
   if (c->code_page_stride < rows * c->head_dim / 2 || c->scale_page_stride < rows * c->head_dim / 16 ||
-      c->code_page_stride > kMaxStride || c->scale_page_stride > kMaxStride)
+      c->code_page_stride > kMaxPageStride || c->scale_page_stride > kMaxPageStride)
     return NVFP4_ERR_SHAPE;
   if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
       !aligned(c->v_scales, 16) || c->code_page_stride % 16 != 0 || c->scale_page_stride % 16 != 0 ||

@@ -605,7 +605,8 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* S
  *   page_size   a power of two, 16 .. 65536.
  *   head_dim    a multiple of 16 up to 1024 (attention: 64 or 128).
  *   k_codes, k_scales, v_codes, v_scales and their strides are 16-byte
- *   aligned; the strides are at least a page's bytes; S is 4-byte aligned.
+ *   aligned; the strides are at least a page's bytes and below 2^32; S is
+ *   4-byte aligned.
  * The struct is read during the call and may be reused at once.
  * ------------------------------------------------------------------------ */
 typedef struct nvfp4_kv_cache {
