@@ -36,8 +36,7 @@
 // first and its last item), which kv_join_kernel adds up.
 #include <type_traits>
 
-#include "kv_cache.cuh"
-#include "nvfp4_device.cuh"
+#include "kv_attention.cuh"
 
 namespace nvfp4 {
 
@@ -51,7 +50,8 @@ constexpr int kStages = 2;   // tiles of a warp's ring
 // What starting and finishing an item costs a CTA, in tiles: its page ids and
 // queries arrive in two trips to memory, its warps meet twice at the end.
 constexpr int kItemCost = 8;
-constexpr float kSlack = 8.0f;  // log2 by which a score may pass the running maximum
+// Query rows of a sequence and KV head up to which this kernel serves it.
+constexpr int64_t kRowsLimit = 32;
 
 // Resident CTAs the kernel is built for (its registers and shared memory).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : (nt == 2 ? 4 : 2); }
@@ -65,18 +65,6 @@ __host__ __device__ constexpr int rows_smem(int D, int NT) {
   return use > join ? use : join;
 }
 
-struct Params {
-  KvAttention a;
-  int group, page_shift;
-  float scale_log2;
-  float* partial;  // [CTA][2][R * D] sums, then [CTA][2][R * 2] maximum and sum
-  float* partial_ml;
-  int ctas;
-};
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // 16 bytes to shared memory, or 16 zeros where `bytes` is 0.
 template <int kDst, int kSrc>
 __device__ __forceinline__ void copy16(uint32_t dst, uint64_t src, int bytes) {
@@ -90,32 +78,6 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
-// low half of r[i].
-__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&r)[4]) {
-  asm("{ .reg .b8 a, b, c, d;\n"
-      "mov.b32 {a, b, c, d}, %4;\n"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
-      "cvt.rn.f16x2.e2m1x2 %3, d; }"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -126,37 +88,23 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float to_f32(uint16_t v, int type) {
-  return type == kBf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
-                       : __half2float(__ushort_as_half(v));
-}
-
 // What the schedule knows of one sequence.
-struct Seq {
-  int q0, lq, lk;     // first query row, new tokens, cached tokens
+struct Seq : Span {
   int t0, tiles;      // first tile that a query sees, tiles per item (at least 1)
   int span;           // units of an item on the line of work: kItemCost, then its tiles
-  int blocks;         // row blocks
+  int blocks;         // row blocks (0: no rows, or the other kernel's)
 };
 
 template <int R>
 __device__ __forceinline__ Seq sequence(const Params& p, int b) {
   Seq s;
-  const int lo = p.a.q_offsets[b], hi = p.a.q_offsets[b + 1];
-  s.q0 = min(max(lo, 0), p.a.total_q);
-  s.lq = min(min(max(hi, s.q0), p.a.total_q) - s.q0, p.a.max_q);
-  s.lk = min(max(p.a.kv_lengths[b], 0), p.a.max_kv);
+  static_cast<Span&>(s) = span_of(p, b);
   const int first = p.a.window > 0 ? max(0, s.lk - s.lq - p.a.window + 1) : 0;
   s.t0 = first / kTile;
   s.tiles = max(1, (s.lk + kTile - 1) / kTile - s.t0);
   s.span = s.tiles + kItemCost;
-  s.blocks = (s.lq * p.group + R - 1) / R;
+  const int rows = s.lq * p.group;
+  s.blocks = rows > p.rows_limit ? 0 : (rows + R - 1) / R;
   return s;
 }
 
@@ -191,40 +139,6 @@ __device__ __forceinline__ long long units_before(const Params& p, int n, long l
 __device__ __forceinline__ long long units_per_cta(long long total, int ctas) {
   const long long share = (total + ctas - 1) / ctas;
   return share > kWarps + kItemCost ? share : kWarps + kItemCost;
-}
-
-// A row r of a block of a sequence: query r / G, head h G + r % G.
-__device__ __forceinline__ void visible(const Params& p, const Seq& s, int row, int& lo, int& hi) {
-  if (row >= s.lq * p.group) {
-    lo = hi = 0;
-    return;
-  }
-  const int pos = s.lk - s.lq + row / p.group;
-  hi = p.a.causal ? min(s.lk, pos + 1) : s.lk;
-  lo = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0;
-}
-
-__device__ __forceinline__ void write_row(const Params& p, const Seq& s, int h, int row, int d, float4 v,
-                                          float inv) {
-  const int64_t t = s.q0 + row / p.group;
-  const int64_t head = h * p.group + row % p.group;
-  uint16_t* o = static_cast<uint16_t*>(p.a.out) + t * p.a.o_token_stride + head * p.a.o_head_stride + d;
-  uint2 w;
-  if (p.a.type == kBf16) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v.y * inv), "f"(v.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v.w * inv), "f"(v.z * inv));
-  } else {
-    w.x = pack_f16x2(v.x * inv, v.y * inv);
-    w.y = pack_f16x2(v.z * inv, v.w * inv);
-  }
-  *reinterpret_cast<uint2*>(o) = w;
-}
-
-__device__ __forceinline__ void write_lse(const Params& p, const Seq& s, int h, int row, float m, float l) {
-  if (p.a.lse == nullptr) return;
-  const int64_t t = s.q0 + row / p.group;
-  p.a.lse[t * p.a.q_heads + h * p.group + row % p.group] =
-      l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 template <int D, int NT>
@@ -411,15 +325,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       for (int i = 0; i < KW * 8; ++i) mx = fmaxf(mx, fabsf(y[i]));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      // power of two at or below the maximum, kept where its reciprocal is a
-      // normal number; Inf and NaN stay what they are in FP16
-      const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-      float shrink = __uint_as_float((254u - e) << 23);
-      float fs = __uint_as_float(e << 23) * p.scale_log2 * c.k_S[h];
-      // the factor is kept above 0 (a negative one turns Q's sign), so that
-      // it keeps the order of scores and a hidden score's -inf
-      if (fs < 0.0f) fs = -fs, shrink = -shrink;
-      if (fs < 0x1p-120f) fs = 0x1p-120f;
+      float shrink, fs;
+      row_scale(mx, p.scale_log2 * c.k_S[h], shrink, fs);
 #pragma unroll
       for (int w = 0; w < KW; ++w)
         q[(n * KW + w) * 32] = make_uint4(pack_f16x2(y[8 * w] * shrink, y[8 * w + 1] * shrink),
@@ -768,22 +675,34 @@ int log2_of(int v) {
 }
 
 // Rows per item: the fewest 8-row tiles that hold all rows of a sequence.
-int row_tiles(int64_t max_q, int q_heads, int kv_heads) {
-  const int64_t rows = max_q * (q_heads / kv_heads);
-  return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-}
+int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 
-int row_ctas(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int nt, int num_sms) {
-  const int64_t blocks = (max_q * (q_heads / kv_heads) + 8 * nt - 1) / (8 * nt);
-  const double tiles = static_cast<double>(batch) * blocks * kv_heads *
+// How a call is served: sequences of at most `limit` query rows for a KV head
+// by kv_rows_kernel, the others by kv_prompt_kernel.
+struct Plan {
+  int64_t rows;   // most rows that kv_rows_kernel gets of a sequence
+  int nt, ctas;   // its 8-row tiles and CTAs
+  int limit;
+  bool prompt;
+};
+
+Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int num_sms) {
+  Plan p;
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  p.prompt = rows > kRowsLimit;
+  p.limit = p.prompt ? kRowsLimit : 0x7FFFFFFF;
+  p.rows = p.prompt ? kRowsLimit : rows;
+  p.nt = row_tiles(p.rows);
+  const double tiles = static_cast<double>(batch) * kv_heads * static_cast<double>((p.rows + 8 * p.nt - 1) / (8 * p.nt)) *
                        static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
-  const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(nt);
+  const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(p.nt);
   const double want = tiles / (kWarps + kItemCost) + 1.0;
-  return static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
+  p.ctas = static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
+  return p;
 }
 
 template <int D, int NT>
-cudaError_t run_rows(Params& p, cudaStream_t stream) {
+cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
   constexpr int R = 8 * NT;
   constexpr int smem = rows_smem(D, NT);
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_rows_kernel<D, NT>),
@@ -793,7 +712,7 @@ cudaError_t run_rows(Params& p, cudaStream_t stream) {
   kv_rows_kernel<D, NT><<<p.ctas, kThreads, smem, stream>>>(p);
   cudaError_t r = cudaGetLastError();
   if (r != cudaSuccess) return r;
-  const int blocks = (p.a.max_q * p.group + R - 1) / R;
+  const int blocks = static_cast<int>((plan.rows + R - 1) / R);
   const dim3 grid(static_cast<unsigned>(blocks) * p.a.c.kv_heads * R, static_cast<unsigned>(p.a.batch));
   kv_join_kernel<D, NT><<<grid, kThreads, 0, stream>>>(p, blocks);
   return cudaGetLastError();
@@ -803,29 +722,33 @@ cudaError_t run_rows(Params& p, cudaStream_t stream) {
 
 size_t kv_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                     int kv_heads, int head_dim, int num_sms) {
-  const int nt = row_tiles(max_q, q_heads, kv_heads);
-  const int ctas = row_ctas(batch, max_q, max_kv, q_heads, kv_heads, nt, num_sms);
-  return static_cast<size_t>(ctas) * 2 * 8 * nt * (head_dim + 2) * sizeof(float);
+  const Plan p = plan_of(batch, max_q, max_kv, q_heads, kv_heads, num_sms);
+  return static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_sms, cudaStream_t stream) {
   if (a.batch == 0 || a.total_q == 0) return cudaSuccess;
+  const Plan plan = plan_of(a.batch, a.max_q, a.max_kv, a.q_heads, a.c.kv_heads, num_sms);
   Params p{};
   p.a = a;
   p.group = a.q_heads / a.c.kv_heads;
-  p.page_shift = log2_of(a.c.page_size);
+  while ((1 << p.page_shift) < a.c.page_size) ++p.page_shift;
   p.scale_log2 = a.scale * 1.44269504088896341f;
   p.partial = static_cast<float*>(workspace);
-  const int nt = row_tiles(a.max_q, a.q_heads, a.c.kv_heads);
-  p.ctas = row_ctas(a.batch, a.max_q, a.max_kv, a.q_heads, a.c.kv_heads, nt, num_sms);
-  if (a.c.head_dim == 128) {
-    if (nt == 1) return run_rows<128, 1>(p, stream);
-    if (nt == 2) return run_rows<128, 2>(p, stream);
-    return run_rows<128, 4>(p, stream);
+  p.ctas = plan.ctas;
+  p.rows_limit = plan.limit;
+  if (plan.prompt) {
+    const cudaError_t e = launch_kv_prompt(p, stream);
+    if (e != cudaSuccess) return e;
   }
-  if (nt == 1) return run_rows<64, 1>(p, stream);
-  if (nt == 2) return run_rows<64, 2>(p, stream);
-  return run_rows<64, 4>(p, stream);
+  if (a.c.head_dim == 128) {
+    if (plan.nt == 1) return run_rows<128, 1>(p, plan, stream);
+    if (plan.nt == 2) return run_rows<128, 2>(p, plan, stream);
+    return run_rows<128, 4>(p, plan, stream);
+  }
+  if (plan.nt == 1) return run_rows<64, 1>(p, plan, stream);
+  if (plan.nt == 2) return run_rows<64, 2>(p, plan, stream);
+  return run_rows<64, 4>(p, plan, stream);
 }
 
 }  // namespace nvfp4

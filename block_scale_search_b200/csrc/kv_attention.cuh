@@ -1,0 +1,129 @@
+// kv_attention.cuh -- what the two attention kernels over the NVFP4 cache share:
+// a call's parameters, number conversions, the mask, and the results' rounding.
+#pragma once
+
+#include "kv_cache.cuh"
+#include "nvfp4_device.cuh"
+
+namespace nvfp4 {
+
+constexpr float kSlack = 8.0f;  // log2 by which a score may pass the running maximum
+
+struct Params {
+  KvAttention a;
+  int group, page_shift;
+  float scale_log2;
+  float* partial;  // [CTA][2][R * D] sums, then [CTA][2][R * 2] maximum and sum
+  float* partial_ml;
+  int ctas;
+  int rows_limit;  // kv_rows_kernel serves sequences with at most so many query rows for a KV head
+  int row_blocks;  // of kv_prompt_kernel
+};
+
+// Prompts (kv_prompt.cu).
+cudaError_t launch_kv_prompt(Params& p, cudaStream_t stream);
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
+// low half of r[i].
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&r)[4]) {
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float to_f32(uint16_t v, int type) {
+  return type == kBf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
+                       : __half2float(__ushort_as_half(v));
+}
+
+// Scaling of a query row whose largest magnitude is mx: the row goes to FP16
+// times `shrink`, a power of two that puts its maximum into [1, 2) (where the
+// reciprocal is a normal number); Inf and NaN stay what they are.  `factor`
+// turns a dot product into a score in base 2.  It is kept above 0 (a negative
+// one turns the row's sign), so that it keeps the order of scores and a hidden
+// score's -inf.
+__device__ __forceinline__ void row_scale(float mx, float scale, float& shrink, float& factor) {
+  const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+  shrink = __uint_as_float((254u - e) << 23);
+  factor = __uint_as_float(e << 23) * scale;
+  if (factor < 0.0f) factor = -factor, shrink = -shrink;
+  if (factor < 0x1p-120f) factor = 0x1p-120f;
+}
+
+// One sequence: its first query row, new tokens and cached tokens, whatever the
+// device arrays hold brought into the call's bounds.
+struct Span {
+  int q0, lq, lk;
+};
+__device__ __forceinline__ Span span_of(const Params& p, int b) {
+  Span s;
+  const int lo = p.a.q_offsets[b], hi = p.a.q_offsets[b + 1];
+  s.q0 = min(max(lo, 0), p.a.total_q);
+  s.lq = min(min(max(hi, s.q0), p.a.total_q) - s.q0, p.a.max_q);
+  s.lk = min(max(p.a.kv_lengths[b], 0), p.a.max_kv);
+  return s;
+}
+
+// Tokens [lo, hi) that row `row` of a sequence (query row / G, head h G + row % G)
+// may see; none behind its last row.
+__device__ __forceinline__ void visible(const Params& p, const Span& s, int row, int& lo, int& hi) {
+  if (row >= s.lq * p.group) {
+    lo = hi = 0;
+    return;
+  }
+  const int pos = s.lk - s.lq + row / p.group;
+  hi = p.a.causal ? min(s.lk, pos + 1) : s.lk;
+  lo = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0;
+}
+
+__device__ __forceinline__ void write_row(const Params& p, const Span& s, int h, int row, int d, float4 v,
+                                          float inv) {
+  const int64_t t = s.q0 + row / p.group;
+  const int64_t head = h * p.group + row % p.group;
+  uint16_t* o = static_cast<uint16_t*>(p.a.out) + t * p.a.o_token_stride + head * p.a.o_head_stride + d;
+  uint2 w;
+  if (p.a.type == kBf16) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v.y * inv), "f"(v.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v.w * inv), "f"(v.z * inv));
+  } else {
+    w.x = pack_f16x2(v.x * inv, v.y * inv);
+    w.y = pack_f16x2(v.z * inv, v.w * inv);
+  }
+  *reinterpret_cast<uint2*>(o) = w;
+}
+
+__device__ __forceinline__ void write_lse(const Params& p, const Span& s, int h, int row, float m, float l) {
+  if (p.a.lse == nullptr) return;
+  const int64_t t = s.q0 + row / p.group;
+  p.a.lse[t * p.a.q_heads + h * p.group + row % p.group] =
+      l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+}  // namespace nvfp4

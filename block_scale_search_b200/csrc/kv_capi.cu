@@ -11,7 +11,7 @@
 
 namespace nvfp4 {
 int record_cuda_status(cudaError_t e);
-unsigned int kv_stalls(bool reset, cudaError_t* e) { (void)reset; *e = cudaSuccess; return 0; }
+unsigned int kv_stalls(bool reset, cudaError_t* e);
 }  // namespace nvfp4
 
 namespace {

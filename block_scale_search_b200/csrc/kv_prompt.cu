@@ -1,0 +1,540 @@
+// kv_prompt.cu -- attention of many query rows over the paged NVFP4 cache
+// (prompts and prompt chunks), on the tcgen05 tensor cores.
+//
+// One CTA takes 256 query rows (two tiles of 128) of one sequence and KV head
+// and walks the cached tokens 128 at a time:
+//   S = Q K^T     Q, K in shared memory (FP16), S in TMEM (FP32)
+//   P = e^(S - m) S from TMEM to registers and back as FP16 over S's columns
+//   O += P V      P from TMEM, V in shared memory, O in TMEM (FP32)
+// Bound by the tensor cores and the exponentials together: at head_dim 128 a
+// step of 256 x 128 scores is 2048 cycles of MMA at the nominal rate, and
+// 2048 cycles of ex2 at 16 a clock, so all else has to run beside them:
+//   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a thread a row
+//   warps 8-11       decode K and V: packed rows from global memory to FP16
+//                    rows in shared memory, two stages each
+//   warp 12          issues the MMAs: P V of one tile and then Q K^T of its
+//                    next step, in turn with the other tile, so that one
+//                    tile's MMAs run while the other's softmax does
+// The cache is decoded once per CTA: 256 rows share it.  A decoded value (code
+// times scale) is exact in FP16; Q's rows are scaled by powers of two and P is
+// rounded as in kv_attention.cu, and the running maximum moves by the same
+// rule, which leaves O alone in almost every step.
+//
+// K and V rows lie alike: 128-byte rows of 64 elements with the 128-byte
+// swizzle, halves of a row 16 KB apart.  K is the K-major operand of S; of
+// P V, whose inner index are the tokens, the same rows are the MN-major one.
+#include "kv_attention.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kTokens = 128;                // of a step
+constexpr int kTileRows = 128;
+constexpr int kRows = 2 * kTileRows;        // of a CTA
+constexpr int kPromptWarps = 13;
+constexpr int kPromptThreads = 32 * kPromptWarps;
+constexpr int kHalfTile = kTokens * 128;    // bytes: 128 rows of 64 elements
+
+__device__ unsigned int g_stalls;           // waits given up
+
+// Shared memory from a 1024-byte boundary: Q of both tiles, two stages of K,
+// two of V.
+template <int D>
+struct Layout {
+  static constexpr int kTile = kHalfTile * (D / 64);
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBytes = 6 * kTile;
+};
+
+enum Bar : int {
+  kQFull = 0,             // +t: Q of tile t is written
+  kKFull = 2, kKEmpty = 4,  // +stage
+  kVFull = 6, kVEmpty = 8,
+  kSFull = 10,            // +t: S of tile t (and all earlier P V) is done
+  kPFull = 12,            // +t: P of tile t is written
+  kOFull = 14,            // +t: the last P V of tile t is done
+  kScan = 16,             // all V scales were seen
+  kBars = 17
+};
+
+struct Shared {
+  uint64_t bar[kBars];
+  uint32_t tmem;
+  int gave_up;   // a wait was given up: no further one waits
+  int nan_v;     // some visible V scale is NaN
+};
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+// Waits for a phase, for a quarter of a second at most: a wait given up is
+// counted and ends all later ones of the CTA, which then runs to its end.
+__device__ __noinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
+    if (clock64() - t0 > (1ll << 29)) {
+      atomicAdd(&g_stalls, 1u);
+      *reinterpret_cast<volatile int*>(&sh->gave_up) = 1;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_wait(Shared* sh, uint32_t bar, uint32_t parity) {
+  if (!mbar_try(bar, parity)) mbar_wait_slow(sh, bar, parity);
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Operand descriptor: 128-byte swizzle, groups of 8 rows 1024 bytes apart;
+// `lead` is the distance of 64-element halves (used by the MN-major operand).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+// FP16 operands, FP32 sums, 128 rows, n columns; b_mn: B's outer index is contiguous.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(add ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(add ? 1 : 0)
+      : "memory");
+}
+
+#define NVFP4_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define NVFP4_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : NVFP4_R8(r, 0), NVFP4_R8(r, 8), NVFP4_R8(r, 16), NVFP4_R8(r, 24) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::NVFP4_I8(r, 0), NVFP4_I8(r, 8), NVFP4_I8(r, 16),
+      NVFP4_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::NVFP4_I8(
+          r, 0),
+      NVFP4_I8(r, 8), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#undef NVFP4_R8
+#undef NVFP4_I8
+
+// Byte offset of 16-byte piece `piece` (of D / 8) of row `row` of a tile.
+__device__ __forceinline__ uint32_t tile_at(int row, int piece) {
+  return (piece >> 3) * kHalfTile + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __grid_constant__ Params p) {
+  using L = Layout<D>;
+  extern __shared__ uint8_t dynamic[];
+  __shared__ Shared sh;
+  uint8_t* const smem = dynamic + ((1024 - (smem_u32(dynamic) & 1023)) & 1023);
+  const uint32_t smem_a = smem_u32(smem);
+  const nvfp4_kv_cache& c = p.a.c;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  // the longest items (a sequence's last rows) first
+  const int per_block = p.a.batch * c.kv_heads;
+  const int rb = p.row_blocks - 1 - static_cast<int>(blockIdx.x) / per_block;
+  const int bh = static_cast<int>(blockIdx.x) % per_block;
+  const int b = bh / c.kv_heads, h = bh % c.kv_heads;
+  const Span s = span_of(p, b);
+  const int rows = s.lq * p.group, r0 = rb * kRows;
+  if (rows <= p.rows_limit || r0 >= rows) return;  // the other kernel's, or no rows
+
+  // tokens that some row sees, and the steps over them
+  int lo, hi, unused;
+  visible(p, s, r0, lo, unused);
+  visible(p, s, min(r0 + kRows, rows) - 1, unused, hi);
+  const int first = lo / kTokens;
+  const int steps = hi > lo ? (hi + kTokens - 1) / kTokens - first : 0;
+
+  auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kQFull + t), 128);
+      mbar_init(bar(kKFull + t), 128);
+      mbar_init(bar(kKEmpty + t), 1);
+      mbar_init(bar(kVFull + t), 128);
+      mbar_init(bar(kVEmpty + t), 1);
+      mbar_init(bar(kSFull + t), 1);
+      mbar_init(bar(kPFull + t), 128);
+      mbar_init(bar(kOFull + t), 1);
+    }
+    mbar_init(bar(kScan), 128);
+    sh.gave_up = 0;
+    sh.nan_v = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {  // all of TMEM: one CTA an SM
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  // columns: S (P over its first half) of tile t at 128 t, O at 256 + D t
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2, row = r0 + t * kTileRows + (threadIdx.x & 127);
+    const bool have = row < rows;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
+    const uint32_t s_col = tmem + lane_base + 128 * t, o_col = tmem + lane_base + 256 + D * t;
+    float f;  // factor of the row's scores, base 2
+    {
+      const uint16_t* src = static_cast<const uint16_t*>(p.a.Q) +
+                            (s.q0 + (have ? row : r0) / p.group) * p.a.q_token_stride +
+                            static_cast<int64_t>(h * p.group + (have ? row : r0) % p.group) * p.a.q_head_stride;
+      uint4 v[D / 8];
+      float mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        v[i] = have ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mx = fmaxf(mx, fmaxf(fabsf(to_f32(w[j] & 0xFFFFu, p.a.type)), fabsf(to_f32(w[j] >> 16, p.a.type))));
+      }
+      float shrink;
+      row_scale(mx, p.scale_log2 * c.k_S[h], shrink, f);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = pack_f16x2(to_f32(w[j] & 0xFFFFu, p.a.type) * shrink, to_f32(w[j] >> 16, p.a.type) * shrink);
+        *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + tile_at(threadIdx.x & 127, i)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_async();
+      mbar_arrive(bar(kQFull + t));
+    }
+    int vlo, vhi;
+    visible(p, s, row, vlo, vhi);
+    // tokens that all rows of the tile see
+    int all_lo, all_hi, x0, x1;
+    visible(p, s, min(r0 + t * kTileRows, rows - 1), x0, all_hi);
+    visible(p, s, min(r0 + (t + 1) * kTileRows, rows) - 1, all_lo, x1);
+    const int* const row_table = p.a.table + b * p.a.table_stride;
+    // lane i < 8: does the page of tokens 16 i .. of a step exist?
+    auto gone = [&](int i) {
+      const int tok = (first + i) * kTokens + 16 * lane;
+      if (lane >= 8 || i >= steps || tok >= s.lk) return false;
+      const int id = row_table[tok >> p.page_shift];
+      return id < 0 || id >= c.num_pages;
+    };
+    bool next_gone = gone(0);
+    float m = -INFINITY, down = 0.0f, l = 0.0f;
+    for (int i = 0; i < steps; ++i) {
+      const int tb = (first + i) * kTokens;
+      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, next_gone);
+      next_gone = gone(i + 1);
+      const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
+      mbar_wait(&sh, bar(kSFull + t), i & 1);
+      tc_fence_after();
+      uint32_t x[32];
+      auto hide = [&](int q) {  // hidden scores of 32 columns become -inf
+        if (!edge) return;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int tk = tb + 32 * q + j;
+          if (tk < vlo || tk >= vhi || ((dead >> (2 * q + j / 16)) & 1)) x[j] = 0xFF800000u;
+        }
+      };
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        tmem_load32(s_col + 32 * q, x);
+        tmem_wait_load();
+        hide(q);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+      }
+      mx *= f;
+      if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+        const float top = fmaxf(m, mx);
+        const float r = top == m ? 1.0f : exp2_approx(m - top);
+        m = top;
+        down = top == -INFINITY ? 0.0f : -top;
+        l *= r;
+        if (i > 0) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            tmem_load32(o_col + 32 * q, x);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * r);
+            tmem_store32(o_col + 32 * q, x);
+          }
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        tmem_load32(s_col + 32 * q, x);
+        tmem_wait_load();
+        hide(q);
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float a = exp2_approx(fmaf(__uint_as_float(x[2 * j]), f, down));
+          const float z = exp2_approx(fmaf(__uint_as_float(x[2 * j + 1]), f, down));
+          l += a + z;
+          o[j] = pack_f16x2(a, z);
+        }
+        tmem_store16(s_col + 16 * q, o);  // columns that were read before
+      }
+      tmem_wait_store();
+      tc_fence_before();
+      mbar_arrive(bar(kPFull + t));
+    }
+    // -------------------------------------------------------------- result
+    if (steps > 0) {
+      mbar_wait(&sh, bar(kOFull + t), 0);
+      tc_fence_after();
+      mbar_wait(&sh, bar(kScan), 0);
+    }
+    uint32_t nan_blocks = 0;  // bit i: a visible V of elements 16 i .. is NaN
+    if (*reinterpret_cast<volatile int*>(&sh.nan_v) && have) {
+      for (int tk = vlo; tk < vhi; ++tk) {
+        const int id = row_table[tk >> p.page_shift];
+        if (id < 0 || id >= c.num_pages) continue;
+        const uint8_t* sc = c.v_scales + id * c.scale_page_stride +
+                            (static_cast<int64_t>(h) * c.page_size + (tk & (c.page_size - 1))) * (D / 16);
+        for (int i = 0; i < D / 16; ++i) nan_blocks |= (sc[i] & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
+      }
+    }
+    const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      uint32_t x[32];
+      if (steps > 0) {
+        tmem_load32(o_col + 32 * q, x);
+        tmem_wait_load();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = 0;
+      }
+      if (have) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if ((nan_blocks >> (2 * q + j / 16)) & 1) x[j] = 0x7FC00000u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          write_row(p, s, h, row, 32 * q + 4 * j,
+                    make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                                __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])),
+                    inv);
+      }
+    }
+    if (have) write_lse(p, s, h, row, m, l);
+    tc_fence_before();
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- decode
+    // A tile is 128 rows of D / 2 code bytes; a thread takes 16 bytes (32
+    // elements) of D / 32 rows, of K and of V.
+    constexpr int kParts = D / 32, kPieces = kParts;  // 16-byte parts of a row; rows a thread takes
+    const int th = threadIdx.x - 256, part = th % kParts, tr = th / kParts;  // row tr + j 128 / kParts
+    const int* const row_table = p.a.table + b * p.a.table_stride;
+    const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2) + part * 16;
+    const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16) + part * 2;
+    uint4 kw[kPieces], vw[kPieces];
+    uint32_t ks[kPieces], vs[kPieces];
+    bool nan_v = false;
+    auto page_of = [&](int i) {  // lane l < 8: page of tokens 16 l .. of step i, or -1
+      const int tok = (first + i) * kTokens + 16 * lane;
+      if (lane >= 8 || i >= steps || tok >= s.lk) return -1;
+      const int id = row_table[tok >> p.page_shift];
+      return id >= 0 && id < c.num_pages ? id : -1;
+    };
+    int ids = page_of(0);
+    auto fetch = [&](int i) {  // packed rows of step i; zeros where there is no token
+      const int mine = ids;
+      ids = page_of(i + 1);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int row = tr + j * (kTokens / kPieces), tok = (first + i) * kTokens + row;
+        const int id = __shfl_sync(0xFFFFFFFFu, mine, row >> 4);
+        kw[j] = vw[j] = make_uint4(0, 0, 0, 0);
+        ks[j] = vs[j] = 0;
+        if (id >= 0 && tok < s.lk) {
+          const int in_page = tok & (c.page_size - 1);
+          const int64_t co = id * c.code_page_stride + head_codes + in_page * (D / 2);
+          const int64_t so = id * c.scale_page_stride + head_scales + in_page * (D / 16);
+          kw[j] = ld_stream_v4(c.k_codes + co);
+          vw[j] = ld_stream_v4(c.v_codes + co);
+          ks[j] = *reinterpret_cast<const uint16_t*>(c.k_scales + so);
+          vs[j] = *reinterpret_cast<const uint16_t*>(c.v_scales + so);
+        }
+      }
+    };
+    auto write = [&](uint8_t* tile, const uint4 (&w)[kPieces], const uint32_t (&sc)[kPieces]) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int row = tr + j * (kTokens / kPieces);
+        const uint32_t two = e4m3x2_to_f16x2(sc[j]);
+        const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+        const uint32_t wv[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        uint4 out[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t e[4];
+          decode_word(wv[u], e);
+          const uint32_t sx = u < 2 ? s0 : s1;
+          out[u] = make_uint4(mul_f16x2(e[0], sx), mul_f16x2(e[1], sx), mul_f16x2(e[2], sx), mul_f16x2(e[3], sx));
+        }
+        // lanes of both halves of a row start at different pieces, so that
+        // eight lanes cover all banks
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bool flip = part & 2;
+          const uint4 val = flip ? out[u ^ 2] : out[u];
+          *reinterpret_cast<uint4*>(tile + tile_at(row, part * 4 + (flip ? u ^ 2 : u))) = val;
+        }
+      }
+    };
+    if (steps > 0) fetch(0);
+    for (int i = 0; i < steps; ++i) {
+      const int st = i & 1, use = i >> 1;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        // 0 * NaN would reach rows that do not see the token: NaN is taken
+        // out of the product, and the rows that see it look for it at the end
+        if ((vs[j] & 0x7Fu) == 0x7Fu) nan_v = true, vs[j] &= 0xFF00u;
+        if ((vs[j] & 0x7F00u) == 0x7F00u) nan_v = true, vs[j] &= 0x00FFu;
+      }
+      mbar_wait(&sh, bar(kKEmpty + st), (use & 1) ^ 1);
+      write(smem + L::kK + st * L::kTile, kw, ks);
+      fence_async();
+      mbar_arrive(bar(kKFull + st));
+      mbar_wait(&sh, bar(kVEmpty + st), (use & 1) ^ 1);
+      write(smem + L::kV + st * L::kTile, vw, vs);
+      fence_async();
+      mbar_arrive(bar(kVFull + st));
+      if (i + 1 < steps) fetch(i + 1);
+    }
+    if (nan_v) *reinterpret_cast<volatile int*>(&sh.nan_v) = 1;
+    mbar_arrive(bar(kScan));
+  } else if (steps > 0) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t kQk = mma_desc(kTokens, false), kPv = mma_desc(D, true);
+      auto qk = [&](int t, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * kHalfTile + (k & 3) * 32;
+          mma_ss(tmem + 128 * t, smem_desc(smem_a + L::kQ + t * L::kTile + at, 16),
+                 smem_desc(smem_a + L::kK + st * L::kTile + at, 16), kQk, k > 0);
+        }
+        tc_commit(bar(kSFull + t));
+      };
+      mbar_wait(&sh, bar(kKFull), 0);
+      for (int t = 0; t < 2; ++t) {
+        mbar_wait(&sh, bar(kQFull + t), 0);
+        tc_fence_after();
+        qk(t, 0);
+      }
+      tc_commit(bar(kKEmpty));
+      for (int i = 0; i < steps; ++i) {
+        const int st = i & 1, nst = (i + 1) & 1;
+        for (int t = 0; t < 2; ++t) {
+          if (t == 0) mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
+          mbar_wait(&sh, bar(kPFull + t), i & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kTokens / 16; ++k)
+            mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k,
+                   smem_desc(smem_a + L::kV + st * L::kTile + k * 2048, kHalfTile), kPv, i > 0 || k > 0);
+          if (i + 1 < steps) {
+            if (t == 0) {
+              mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
+              tc_fence_after();
+            }
+            qk(t, nst);
+          } else {
+            tc_commit(bar(kOFull + t));
+          }
+        }
+        tc_commit(bar(kVEmpty + st));
+        if (i + 1 < steps) tc_commit(bar(kKEmpty + nst));
+      }
+      // nothing of this CTA's is in flight when it ends
+      mbar_wait(&sh, bar(kOFull + 0), 0);
+      mbar_wait(&sh, bar(kOFull + 1), 0);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int D>
+cudaError_t run_prompt(const Params& p, cudaStream_t stream) {
+  constexpr int smem = Layout<D>::kBytes + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_prompt_kernel<D>),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  kv_prompt_kernel<D><<<static_cast<unsigned>(grid), kPromptThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(Params& p, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.a.max_q) * p.group;
+  p.row_blocks = static_cast<int>((rows + kRows - 1) / kRows);
+  return p.a.c.head_dim == 128 ? run_prompt<128>(p, stream) : run_prompt<64>(p, stream);
+}
+
+unsigned int kv_stalls(bool reset, cudaError_t* e) {
+  unsigned int n = 0;
+  *e = cudaMemcpyFromSymbol(&n, g_stalls, sizeof(n));
+  if (*e == cudaSuccess && reset) {
+    const unsigned int z = 0;
+    *e = cudaMemcpyToSymbol(g_stalls, &z, sizeof(z));
+  }
+  return n;
+}
+
+}  // namespace nvfp4
