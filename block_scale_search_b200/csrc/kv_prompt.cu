@@ -15,6 +15,8 @@
 //   warp 12          issues the MMAs: P V of one tile and then Q K^T of its
 //                    next step, in turn with the other tile, so that one
 //                    tile's MMAs run while the other's softmax does
+// Registers move from the last two groups of warps to the softmax, whose
+// threads hold a row's 128 scores at once.
 // The cache is decoded once per CTA: 256 rows share it.  A decoded value (code
 // times scale) is exact in FP16; Q's rows are scaled by powers of two and P is
 // rounded as in kv_attention.cu, and the running maximum moves by the same
@@ -32,7 +34,7 @@ namespace {
 constexpr int kTokens = 128;                // of a step
 constexpr int kTileRows = 128;
 constexpr int kRows = 2 * kTileRows;        // of a CTA
-constexpr int kPromptWarps = 13;
+constexpr int kPromptWarps = 16;
 constexpr int kPromptThreads = 32 * kPromptWarps;
 constexpr int kHalfTile = kTokens * 128;    // bytes: 128 rows of 64 elements
 
@@ -77,11 +79,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
+// The same, suspended for up to 2 us meanwhile.
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done) : "r"(bar), "r"(parity), "r"(2000u) : "memory");
+  return done != 0;
+}
 // Waits for a phase, for a quarter of a second at most: a wait given up is
 // counted and ends all later ones of the CTA, which then runs to its end.
-__device__ __noinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
-  while (!mbar_try(bar, parity)) {
+  while (!mbar_try_long(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
     if (clock64() - t0 > (1ll << 29)) {
       atomicAdd(&g_stalls, 1u);
@@ -100,6 +110,15 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// True in one lane of a converged warp, in a way that the compiler knows to be
+// one lane (a comparison of the lane's number makes it serialise every MMA,
+// whose operands are warp-uniform: 147 cycles each instead of 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
 
 // Operand descriptor: 128-byte swizzle, groups of 8 rows 1024 bytes apart;
 // `lead` is the distance of 64-element halves (used by the MN-major operand).
@@ -135,12 +154,10 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
       "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : NVFP4_R8(r, 0), NVFP4_R8(r, 8), NVFP4_R8(r, 16), NVFP4_R8(r, 24) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::NVFP4_I8(r, 0), NVFP4_I8(r, 8), NVFP4_I8(r, 16),
-      NVFP4_I8(r, 24), "r"(addr)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : NVFP4_R8(r, 0), NVFP4_R8(r, 8) : "r"(addr));
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -212,8 +229,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
   const uint32_t tmem = sh.tmem;
   // columns: S (P over its first half) of tile t at 128 t, O at 256 + D t
 
+  // 128 registers a thread at launch; 128 * (2 * 184 + 96 + 48) are all of them
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int t = warp >> 2, row = r0 + t * kTileRows + (threadIdx.x & 127);
     const bool have = row < rows;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
@@ -270,24 +289,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
       mbar_wait(&sh, bar(kSFull + t), i & 1);
       tc_fence_after();
-      uint32_t x[32];
-      auto hide = [&](int q) {  // hidden scores of 32 columns become -inf
-        if (!edge) return;
+      uint32_t x[4][32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int tk = tb + 32 * q + j;
-          if (tk < vlo || tk >= vhi || ((dead >> (2 * q + j / 16)) & 1)) x[j] = 0xFF800000u;
-        }
-      };
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        tmem_load32(s_col + 32 * q, x);
-        tmem_wait_load();
-        hide(q);
+      for (int q = 0; q < 4; ++q) tmem_load32(s_col + 32 * q, x[q]);
+      tmem_wait_load();
+      if (edge) {  // hidden scores become -inf
+        __syncwarp();  // keeps this a branch
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int tk = tb + 32 * q + j;
+            if (tk < vlo || tk >= vhi || ((dead >> (2 * q + j / 16)) & 1)) x[q][j] = 0xFF800000u;
+          }
       }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[q][j]));
       mx *= f;
       if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
         const float top = fmaxf(m, mx);
@@ -297,29 +317,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         l *= r;
         if (i > 0) {
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            tmem_load32(o_col + 32 * q, x);
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_load16(o_col + 16 * q, o);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * r);
-            tmem_store32(o_col + 32 * q, x);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
+            tmem_store16(o_col + 16 * q, o);
           }
         }
       }
-#pragma unroll 1
+      const f32x2_t f2 = f2_pack(f, f), d2 = f2_pack(down, down);
+      f32x2_t sum = f2_pack(0.0f, 0.0f);
+#pragma unroll
       for (int q = 0; q < 4; ++q) {
-        tmem_load32(s_col + 32 * q, x);
-        tmem_wait_load();
-        hide(q);
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float a = exp2_approx(fmaf(__uint_as_float(x[2 * j]), f, down));
-          const float z = exp2_approx(fmaf(__uint_as_float(x[2 * j + 1]), f, down));
-          l += a + z;
+          float a, z;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2), a, z);
+          a = exp2_approx(a);
+          z = exp2_approx(z);
+          sum = f2_add(sum, f2_pack(a, z));
           o[j] = pack_f16x2(a, z);
         }
-        tmem_store16(s_col + 16 * q, o);  // columns that were read before
+        tmem_store16(s_col + 16 * q, o);  // over scores that are in registers
+      }
+      {
+        float a, z;
+        f2_unpack(sum, a, z);
+        l += a + z;
       }
       tmem_wait_store();
       tc_fence_before();
@@ -368,10 +395,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     tc_fence_before();
   } else if (warp < 12) {
     // ------------------------------------------------------------- decode
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // A tile is 128 rows of D / 2 code bytes; a thread takes 16 bytes (32
-    // elements) of D / 32 rows, of K and of V.
-    constexpr int kParts = D / 32, kPieces = kParts;  // 16-byte parts of a row; rows a thread takes
-    const int th = threadIdx.x - 256, part = th % kParts, tr = th / kParts;  // row tr + j 128 / kParts
+    // elements) of D / 32 rows, of K and of V.  Lanes 2 i and 2 i + 1 take
+    // neighbouring parts of row i of the warp's 16: loads are whole sectors,
+    // and eight lanes' stores cover all banks.
+    constexpr int kPieces = D / 32;
+    const int th = threadIdx.x - 256, wg_warp = warp - 8;
+    const int part = D == 128 ? (th & 1) + 2 * (wg_warp & 1) : th & 1;
+    const int tr = D == 128 ? ((th >> 1) & 15) + 16 * (wg_warp >> 1) : th >> 1;  // row tr + j 128 / kPieces
     const int* const row_table = p.a.table + b * p.a.table_stride;
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2) + part * 16;
     const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16) + part * 2;
@@ -420,14 +452,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
           const uint32_t sx = u < 2 ? s0 : s1;
           out[u] = make_uint4(mul_f16x2(e[0], sx), mul_f16x2(e[1], sx), mul_f16x2(e[2], sx), mul_f16x2(e[3], sx));
         }
-        // lanes of both halves of a row start at different pieces, so that
-        // eight lanes cover all banks
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool flip = part & 2;
-          const uint4 val = flip ? out[u ^ 2] : out[u];
-          *reinterpret_cast<uint4*>(tile + tile_at(row, part * 4 + (flip ? u ^ 2 : u))) = val;
-        }
+        for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(tile + tile_at(row, part * 4 + u)) = out[u];
       }
     };
     if (steps > 0) fetch(0);
@@ -452,16 +478,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     }
     if (nan_v) *reinterpret_cast<volatile int*>(&sh.nan_v) = 1;
     mbar_arrive(bar(kScan));
-  } else if (steps > 0) {
+  } else {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 12 && steps > 0) {
       constexpr uint32_t kQk = mma_desc(kTokens, false), kPv = mma_desc(D, true);
+      const uint64_t q_desc = smem_desc(smem_a + L::kQ, 16), k_desc = smem_desc(smem_a + L::kK, 16),
+                     v_desc = smem_desc(smem_a + L::kV, kHalfTile);
+      constexpr uint64_t kTileStep = L::kTile >> 4;  // in a descriptor's address units
       auto qk = [&](int t, int st) {
+        const uint64_t a = q_desc + t * kTileStep, k0 = k_desc + st * kTileStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k >> 2) * kHalfTile + (k & 3) * 32;
-          mma_ss(tmem + 128 * t, smem_desc(smem_a + L::kQ + t * L::kTile + at, 16),
-                 smem_desc(smem_a + L::kK + st * L::kTile + at, 16), kQk, k > 0);
+          const uint64_t at = ((k >> 2) * kHalfTile + (k & 3) * 32) >> 4;
+          mma_ss(tmem + 128 * t, a + at, k0 + at, kQk, k > 0);
         }
         tc_commit(bar(kSFull + t));
       };
@@ -469,37 +499,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       for (int t = 0; t < 2; ++t) {
         mbar_wait(&sh, bar(kQFull + t), 0);
         tc_fence_after();
-        qk(t, 0);
+        if (elect_one()) qk(t, 0);
+        __syncwarp();
       }
-      tc_commit(bar(kKEmpty));
+      if (elect_one()) tc_commit(bar(kKEmpty));
+      __syncwarp();
       for (int i = 0; i < steps; ++i) {
-        const int st = i & 1, nst = (i + 1) & 1;
+        const int st = i & 1, nst = st ^ 1;
         for (int t = 0; t < 2; ++t) {
           if (t == 0) mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
+          if (t == 0 && i + 1 < steps) mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
           mbar_wait(&sh, bar(kPFull + t), i & 1);
           tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v0 = v_desc + st * kTileStep;
 #pragma unroll
-          for (int k = 0; k < kTokens / 16; ++k)
-            mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k,
-                   smem_desc(smem_a + L::kV + st * L::kTile + k * 2048, kHalfTile), kPv, i > 0 || k > 0);
-          if (i + 1 < steps) {
-            if (t == 0) {
-              mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
-              tc_fence_after();
+            for (int k = 0; k < kTokens / 16; ++k)
+              mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, i > 0 || k > 0);
+            if (i + 1 < steps)
+              qk(t, nst);
+            else
+              tc_commit(bar(kOFull + t));
+            if (t == 1) {
+              tc_commit(bar(kVEmpty + st));
+              if (i + 1 < steps) tc_commit(bar(kKEmpty + nst));
             }
-            qk(t, nst);
-          } else {
-            tc_commit(bar(kOFull + t));
           }
+          __syncwarp();
         }
-        tc_commit(bar(kVEmpty + st));
-        if (i + 1 < steps) tc_commit(bar(kKEmpty + nst));
       }
       // nothing of this CTA's is in flight when it ends
       mbar_wait(&sh, bar(kOFull + 0), 0);
       mbar_wait(&sh, bar(kOFull + 1), 0);
     }
-    __syncwarp();
   }
   __syncthreads();
   tc_fence_after();
