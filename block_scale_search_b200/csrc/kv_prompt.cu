@@ -79,20 +79,15 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
-// The same, suspended for up to 2 us meanwhile.
-__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done) : "r"(bar), "r"(parity), "r"(2000u) : "memory");
-  return done != 0;
-}
 // Waits for a phase, for a quarter of a second at most: a wait given up is
 // counted and ends all later ones of the CTA, which then runs to its end.
 __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_long(bar, parity)) {
+  long long t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try(bar, parity)) return;
+    if ((n & 255u) != 0) continue;  // (a try suspends the thread for a while by itself)
     if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
+    if (t0 == 0) t0 = clock64();
     if (clock64() - t0 > (1ll << 29)) {
       atomicAdd(&g_stalls, 1u);
       *reinterpret_cast<volatile int*>(&sh->gave_up) = 1;
@@ -303,12 +298,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
             if (tk < vlo || tk >= vhi || ((dead >> (2 * q + j / 16)) & 1)) x[q][j] = 0xFF800000u;
           }
       }
-      float mx = -INFINITY;
+      float m4[4];  // chains short enough to overlap
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
+        float a = __uint_as_float(x[q][0]), z = __uint_as_float(x[q][1]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[q][j]));
-      mx *= f;
+        for (int j = 2; j < 32; j += 2) {
+          a = fmaxf(a, __uint_as_float(x[q][j]));
+          z = fmaxf(z, __uint_as_float(x[q][j + 1]));
+        }
+        m4[q] = fmaxf(a, z);
+      }
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
       if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
         const float top = fmaxf(m, mx);
         const float r = top == m ? 1.0f : exp2_approx(m - top);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         }
       }
       const f32x2_t f2 = f2_pack(f, f), d2 = f2_pack(down, down);
-      f32x2_t sum = f2_pack(0.0f, 0.0f);
+      f32x2_t sum[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t o[16];
@@ -338,14 +339,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
           f2_unpack(f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2), a, z);
           a = exp2_approx(a);
           z = exp2_approx(z);
-          sum = f2_add(sum, f2_pack(a, z));
+          sum[j & 3] = f2_add(sum[j & 3], f2_pack(a, z));
           o[j] = pack_f16x2(a, z);
         }
         tmem_store16(s_col + 16 * q, o);  // over scores that are in registers
       }
       {
         float a, z;
-        f2_unpack(sum, a, z);
+        f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, z);
         l += a + z;
       }
       tmem_wait_store();
@@ -407,6 +408,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     const int* const row_table = p.a.table + b * p.a.table_stride;
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2) + part * 16;
     const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16) + part * 2;
+    const uint32_t code_page = static_cast<uint32_t>(c.code_page_stride);
+    const uint32_t scale_page = static_cast<uint32_t>(c.scale_page_stride);
     uint4 kw[kPieces], vw[kPieces];
     uint32_t ks[kPieces], vs[kPieces];
     bool nan_v = false;
@@ -416,27 +419,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       const int id = row_table[tok >> p.page_shift];
       return id >= 0 && id < c.num_pages ? id : -1;
     };
-    int ids = page_of(0);
-    auto fetch = [&](int i) {  // packed rows of step i; zeros where there is no token
-      const int mine = ids;
-      ids = page_of(i + 1);
+    // packed rows of step i, whose pages are `ids`; zeros where there is no token
+    auto fetch = [&](int i, int ids, const uint8_t* codes, const uint8_t* scales, uint4(&w)[kPieces],
+                     uint32_t(&sc)[kPieces]) {
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const int row = tr + j * (kTokens / kPieces), tok = (first + i) * kTokens + row;
-        const int id = __shfl_sync(0xFFFFFFFFu, mine, row >> 4);
-        kw[j] = vw[j] = make_uint4(0, 0, 0, 0);
-        ks[j] = vs[j] = 0;
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, row >> 4);
+        w[j] = make_uint4(0, 0, 0, 0);
+        sc[j] = 0;
         if (id >= 0 && tok < s.lk) {
-          const int in_page = tok & (c.page_size - 1);
-          const int64_t co = id * c.code_page_stride + head_codes + in_page * (D / 2);
-          const int64_t so = id * c.scale_page_stride + head_scales + in_page * (D / 16);
-          kw[j] = ld_stream_v4(c.k_codes + co);
-          vw[j] = ld_stream_v4(c.v_codes + co);
-          ks[j] = *reinterpret_cast<const uint16_t*>(c.k_scales + so);
-          vs[j] = *reinterpret_cast<const uint16_t*>(c.v_scales + so);
+          const uint32_t in_page = tok & (c.page_size - 1);
+          w[j] = ld_stream_v4(codes + static_cast<uint64_t>(static_cast<uint32_t>(id)) * code_page + in_page * (D / 2));
+          sc[j] = *reinterpret_cast<const uint16_t*>(
+              scales + static_cast<uint64_t>(static_cast<uint32_t>(id)) * scale_page + in_page * (D / 16));
         }
       }
     };
+    const uint8_t* const k_codes = c.k_codes + head_codes;
+    const uint8_t* const v_codes = c.v_codes + head_codes;
+    const uint8_t* const k_scales = c.k_scales + head_scales;
+    const uint8_t* const v_scales = c.v_scales + head_scales;
     auto write = [&](uint8_t* tile, const uint4 (&w)[kPieces], const uint32_t (&sc)[kPieces]) {
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
@@ -456,9 +459,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(tile + tile_at(row, part * 4 + u)) = out[u];
       }
     };
-    if (steps > 0) fetch(0);
+    // K of the next step is on its way while V is decoded, and the other way
+    // round; page ids are a step further ahead
+    int ids = page_of(0);
+    if (steps > 0) {
+      fetch(0, ids, k_codes, k_scales, kw, ks);
+      fetch(0, ids, v_codes, v_scales, vw, vs);
+    }
+    ids = page_of(1);
     for (int i = 0; i < steps; ++i) {
       const int st = i & 1, use = i >> 1;
+      const int ids_after = page_of(i + 2);
+      mbar_wait(&sh, bar(kKEmpty + st), (use & 1) ^ 1);
+      write(smem + L::kK + st * L::kTile, kw, ks);
+      fence_async();
+      mbar_arrive(bar(kKFull + st));
+      if (i + 1 < steps) fetch(i + 1, ids, k_codes, k_scales, kw, ks);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         // 0 * NaN would reach rows that do not see the token: NaN is taken
@@ -466,15 +482,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         if ((vs[j] & 0x7Fu) == 0x7Fu) nan_v = true, vs[j] &= 0xFF00u;
         if ((vs[j] & 0x7F00u) == 0x7F00u) nan_v = true, vs[j] &= 0x00FFu;
       }
-      mbar_wait(&sh, bar(kKEmpty + st), (use & 1) ^ 1);
-      write(smem + L::kK + st * L::kTile, kw, ks);
-      fence_async();
-      mbar_arrive(bar(kKFull + st));
       mbar_wait(&sh, bar(kVEmpty + st), (use & 1) ^ 1);
       write(smem + L::kV + st * L::kTile, vw, vs);
       fence_async();
       mbar_arrive(bar(kVFull + st));
-      if (i + 1 < steps) fetch(i + 1);
+      if (i + 1 < steps) fetch(i + 1, ids, v_codes, v_scales, vw, vs);
+      ids = ids_after;
     }
     if (nan_v) *reinterpret_cast<volatile int*>(&sh.nan_v) = 1;
     mbar_arrive(bar(kScan));
