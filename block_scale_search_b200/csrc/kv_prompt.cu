@@ -10,8 +10,8 @@
 // step of 256 x 128 scores is 2048 cycles of MMA at the nominal rate, and
 // 2048 cycles of ex2 at 16 a clock, so all else has to run beside them:
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a thread a row
-//   warps 8-11       decode K and V: packed rows from global memory to FP16
-//                    rows in shared memory, two stages each
+//   warps 8-11       decode K and V: packed rows, which arrive by cp.async two
+//                    half steps ahead, to FP16 rows, two stages each
 //   warp 12          issues the MMAs: P V of one tile and then Q K^T of its
 //                    next step, in turn with the other tile, so that one
 //                    tile's MMAs run while the other's softmax does
@@ -41,11 +41,13 @@ constexpr int kHalfTile = kTokens * 128;    // bytes: 128 rows of 64 elements
 __device__ unsigned int g_stalls;           // waits given up
 
 // Shared memory from a 1024-byte boundary: Q of both tiles, two stages of K,
-// two of V.
+// two of V, and three slots of packed rows (K or V of a step).
 template <int D>
 struct Layout {
   static constexpr int kTile = kHalfTile * (D / 64);
-  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBytes = 6 * kTile;
+  static constexpr int kSlot = kTokens * (D / 2) + kTokens * (D / 32) * 4;
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kPacked = 6 * kTile;
+  static constexpr int kBytes = kPacked + 3 * kSlot;
 };
 
 enum Bar : int {
@@ -53,10 +55,10 @@ enum Bar : int {
   kKFull = 2, kKEmpty = 4,  // +stage
   kVFull = 6, kVEmpty = 8,
   kSFull = 10,            // +t: S of tile t (and all earlier P V) is done
-  kPFull = 12,            // +t: P of tile t is written
-  kOFull = 14,            // +t: the last P V of tile t is done
-  kScan = 16,             // all V scales were seen
-  kBars = 17
+  kPFull = 12,            // +2 t + half: that half of P's columns of tile t is written
+  kOFull = 16,            // +t: the last P V of tile t is done
+  kScan = 18,             // all V scales were seen
+  kBars = 19
 };
 
 struct Shared {
@@ -166,6 +168,45 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 #undef NVFP4_R8
 #undef NVFP4_I8
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Every how many pairs of exponentials one is computed by exp2_poly2.
+constexpr int kPolyEvery = 4;
+
+// 2^x of two numbers on the FMA pipe, beside the ex2 unit's 16 a clock.
+// x = n + r with n whole and |r| <= 1/2: adding 1.5 * 2^23 rounds to n and
+// leaves it in the low bits.  2^r by a quartic (least squares of the relative
+// error, reweighted until it was even: 2.6e-6), n into the exponent.  Below
+// -126 the result stays at 2^-126.
+__device__ __forceinline__ void exp2_poly2(f32x2_t x, float& a, float& z) {
+  f2_unpack(x, a, z);
+  x = f2_pack(fmaxf(a, -126.0f), fmaxf(z, -126.0f));
+  const f32x2_t t = f2_add(x, f2_pack(12582912.0f, 12582912.0f));
+  const f32x2_t n = f2_add(t, f2_pack(-12582912.0f, -12582912.0f));
+  const f32x2_t r = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
+  f32x2_t y = f2_fma(r, f2_pack(0.00957010128f, 0.00957010128f), f2_pack(0.0559178603f, 0.0559178603f));
+  y = f2_fma(y, r, f2_pack(0.240247448f, 0.240247448f));
+  y = f2_fma(y, r, f2_pack(0.693121815f, 0.693121815f));
+  y = f2_fma(y, r, f2_pack(0.999999261f, 0.999999261f));
+  float ta, tz, ya, yz;
+  f2_unpack(t, ta, tz);
+  f2_unpack(y, ya, yz);
+  a = __uint_as_float((__float_as_uint(ta) << 23) + __float_as_uint(ya));
+  z = __uint_as_float((__float_as_uint(tz) << 23) + __float_as_uint(yz));
+}
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, uint64_t src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Byte offset of 16-byte piece `piece` (of D / 8) of row `row` of a tile.
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (piece >> 3) * kHalfTile + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
@@ -206,7 +247,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       mbar_init(bar(kVFull + t), 128);
       mbar_init(bar(kVEmpty + t), 1);
       mbar_init(bar(kSFull + t), 1);
-      mbar_init(bar(kPFull + t), 128);
+      mbar_init(bar(kPFull + 2 * t), 128);
+      mbar_init(bar(kPFull + 2 * t + 1), 128);
       mbar_init(bar(kOFull + t), 1);
     }
     mbar_init(bar(kScan), 128);
@@ -268,19 +310,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     visible(p, s, min(r0 + t * kTileRows, rows - 1), x0, all_hi);
     visible(p, s, min(r0 + (t + 1) * kTileRows, rows) - 1, all_lo, x1);
     const int* const row_table = p.a.table + b * p.a.table_stride;
-    // lane i < 8: does the page of tokens 16 i .. of a step exist?
-    auto gone = [&](int i) {
+    // lane i < 8: the table's entry for tokens 16 i .. of a step (0 if none is
+    // needed), loaded a step before it is looked at
+    auto page_of = [&](int i) {
       const int tok = (first + i) * kTokens + 16 * lane;
-      if (lane >= 8 || i >= steps || tok >= s.lk) return false;
-      const int id = row_table[tok >> p.page_shift];
-      return id < 0 || id >= c.num_pages;
+      return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : 0;
     };
-    bool next_gone = gone(0);
+    int page = page_of(0);
     float m = -INFINITY, down = 0.0f, l = 0.0f;
     for (int i = 0; i < steps; ++i) {
       const int tb = (first + i) * kTokens;
-      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, next_gone);
-      next_gone = gone(i + 1);
+      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
+      page = page_of(i + 1);
       const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
       mbar_wait(&sh, bar(kSFull + t), i & 1);
       tc_fence_after();
@@ -298,20 +339,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
             if (tk < vlo || tk >= vhi || ((dead >> (2 * q + j / 16)) & 1)) x[q][j] = 0xFF800000u;
           }
       }
+      // a NaN score has to reach m: not every exponential below would keep it
       float m4[4];  // chains short enough to overlap
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float a = __uint_as_float(x[q][0]), z = __uint_as_float(x[q][1]);
 #pragma unroll
-        for (int j = 2; j < 32; j += 2) {
-          a = fmaxf(a, __uint_as_float(x[q][j]));
-          z = fmaxf(z, __uint_as_float(x[q][j + 1]));
+        for (int j = 2; j < 32; j += 4) {
+          a = max3_nan(a, __uint_as_float(x[q][j]), __uint_as_float(x[q][j + 1]));
+          if (j + 3 < 32) z = max3_nan(z, __uint_as_float(x[q][j + 2]), __uint_as_float(x[q][j + 3]));
         }
-        m4[q] = fmaxf(a, z);
+        m4[q] = max3_nan(a, z, z);
       }
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
-      if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-        const float top = fmaxf(m, mx);
+      const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * f;
+      if (__any_sync(0xFFFFFFFFu, !(mx <= m + kSlack))) {
+        const float top = max3_nan(m, mx, mx);
         const float r = top == m ? 1.0f : exp2_approx(m - top);
         m = top;
         down = top == -INFINITY ? 0.0f : -top;
@@ -335,14 +377,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
+          const f32x2_t y = f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2);
           float a, z;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2), a, z);
-          a = exp2_approx(a);
-          z = exp2_approx(z);
+          if (j % kPolyEvery == kPolyEvery - 1) {
+            exp2_poly2(y, a, z);
+          } else {
+            f2_unpack(y, a, z);
+            a = exp2_approx(a);
+            z = exp2_approx(z);
+          }
           sum[j & 3] = f2_add(sum[j & 3], f2_pack(a, z));
           o[j] = pack_f16x2(a, z);
         }
         tmem_store16(s_col + 16 * q, o);  // over scores that are in registers
+        if (q == 1) {  // P V may begin
+          tmem_wait_store();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + 2 * t));
+        }
       }
       {
         float a, z;
@@ -351,7 +403,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       }
       tmem_wait_store();
       tc_fence_before();
-      mbar_arrive(bar(kPFull + t));
+      mbar_arrive(bar(kPFull + 2 * t + 1));
     }
     // -------------------------------------------------------------- result
     if (steps > 0) {
@@ -369,6 +421,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int i = 0; i < D / 16; ++i) nan_blocks |= (sc[i] & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
       }
     }
+    if (m == -INFINITY) l = 0.0f;  // saw no token (the sum may hold some 2^-126)
     const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
@@ -407,87 +460,107 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     const int tr = D == 128 ? ((th >> 1) & 15) + 16 * (wg_warp >> 1) : th >> 1;  // row tr + j 128 / kPieces
     const int* const row_table = p.a.table + b * p.a.table_stride;
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2) + part * 16;
-    const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16) + part * 2;
+    // (a row's scales are copied four at a time)
+    const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16) + (part >> 1) * 4;
     const uint32_t code_page = static_cast<uint32_t>(c.code_page_stride);
     const uint32_t scale_page = static_cast<uint32_t>(c.scale_page_stride);
-    uint4 kw[kPieces], vw[kPieces];
-    uint32_t ks[kPieces], vs[kPieces];
-    bool nan_v = false;
-    auto page_of = [&](int i) {  // lane l < 8: page of tokens 16 l .. of step i, or -1
+    const uint64_t k_codes = reinterpret_cast<uint64_t>(c.k_codes + head_codes);
+    const uint64_t v_codes = reinterpret_cast<uint64_t>(c.v_codes + head_codes);
+    const uint64_t k_scales = reinterpret_cast<uint64_t>(c.k_scales + head_scales);
+    const uint64_t v_scales = reinterpret_cast<uint64_t>(c.v_scales + head_scales);
+    // A thread copies what it will decode, so nobody else waits for it:
+    // codes at slot + (j 128 + th) 16, scales behind them at (j 128 + th) 4.
+    const uint32_t packed = smem_a + L::kPacked;
+    auto page_of = [&](int i) {  // lane l < 8: the table's entry for tokens 16 l .. of step i, or -1
       const int tok = (first + i) * kTokens + 16 * lane;
-      if (lane >= 8 || i >= steps || tok >= s.lk) return -1;
-      const int id = row_table[tok >> p.page_shift];
-      return id >= 0 && id < c.num_pages ? id : -1;
+      return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : -1;
     };
-    // packed rows of step i, whose pages are `ids`; zeros where there is no token
-    auto fetch = [&](int i, int ids, const uint8_t* codes, const uint8_t* scales, uint4(&w)[kPieces],
-                     uint32_t(&sc)[kPieces]) {
+    // starts the copy of K or V of step i, whose pages are `ids`, to a slot;
+    // returns bit j: the row of piece j is a cached token (the others are any
+    // row, to be given scale 0)
+    auto request = [&](int i, int ids, uint64_t codes, uint64_t scales, uint32_t slot) {
+      uint32_t there = 0;
+      if (i < steps) {
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int row = tr + j * (kTokens / kPieces), tok = (first + i) * kTokens + row;
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, row >> 4);
-        w[j] = make_uint4(0, 0, 0, 0);
-        sc[j] = 0;
-        if (id >= 0 && tok < s.lk) {
+        for (int j = 0; j < kPieces; ++j) {
+          const int row = tr + j * (kTokens / kPieces), tok = (first + i) * kTokens + row;
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, row >> 4);
+          const bool ok = id >= 0 && id < c.num_pages && tok < s.lk;
+          const uint64_t page = static_cast<uint32_t>(ok ? id : 0);
           const uint32_t in_page = tok & (c.page_size - 1);
-          w[j] = ld_stream_v4(codes + static_cast<uint64_t>(static_cast<uint32_t>(id)) * code_page + in_page * (D / 2));
-          sc[j] = *reinterpret_cast<const uint16_t*>(
-              scales + static_cast<uint64_t>(static_cast<uint32_t>(id)) * scale_page + in_page * (D / 16));
+          there |= ok ? 1u << j : 0u;
+          copy_async<16>(packed + slot + (j * 128 + th) * 16, codes + page * code_page + in_page * (D / 2));
+          copy_async<4>(packed + slot + kTokens * (D / 2) + (j * 128 + th) * 4,
+                        scales + page * scale_page + in_page * (D / 16));
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return there;
     };
-    const uint8_t* const k_codes = c.k_codes + head_codes;
-    const uint8_t* const v_codes = c.v_codes + head_codes;
-    const uint8_t* const k_scales = c.k_scales + head_scales;
-    const uint8_t* const v_scales = c.v_scales + head_scales;
-    auto write = [&](uint8_t* tile, const uint4 (&w)[kPieces], const uint32_t (&sc)[kPieces]) {
+    uint32_t at[4];  // of a row's four pieces in a tile; rows are 8 k apart, so the swizzle stays
+#pragma unroll
+    for (int u = 0; u < 4; ++u) at[u] = tile_at(tr, part * 4 + u);
+    // decodes a slot's rows into a tile, once the tile's last use is over
+    bool nan_v = false;
+    auto decode = [&](uint32_t slot, uint32_t there, bool isv, int bar_empty, uint32_t parity, uint8_t* tile) {
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      const uint8_t* const from = smem + L::kPacked + slot;
+      uint4 w[kPieces];
+      uint32_t sc[kPieces], odd = 0;
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        const int row = tr + j * (kTokens / kPieces);
+        w[j] = *reinterpret_cast<const uint4*>(from + (j * 128 + th) * 16);
+        sc[j] = *reinterpret_cast<const uint32_t*>(from + kTokens * (D / 2) + (j * 128 + th) * 4);
+        if (part & 1) sc[j] >>= 16;
+        sc[j] = (there >> j) & 1 ? sc[j] & 0xFFFFu : 0u;
+        odd |= ((sc[j] & 0x7F7Fu) + 0x0101u) & 0x8080u;
+      }
+      if (isv && odd) {
+        // 0 * NaN would reach rows that do not see the token: NaN is taken out
+        // of the product, and the rows that see it look for it at the end
+        nan_v = true;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          if ((sc[j] & 0x7Fu) == 0x7Fu) sc[j] &= 0xFF00u;
+          if ((sc[j] & 0x7F00u) == 0x7F00u) sc[j] &= 0x00FFu;
+        }
+      }
+      mbar_wait(&sh, bar(bar_empty), parity);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
         const uint32_t two = e4m3x2_to_f16x2(sc[j]);
         const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
         const uint32_t wv[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        uint4 out[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t e[4];
           decode_word(wv[u], e);
           const uint32_t sx = u < 2 ? s0 : s1;
-          out[u] = make_uint4(mul_f16x2(e[0], sx), mul_f16x2(e[1], sx), mul_f16x2(e[2], sx), mul_f16x2(e[3], sx));
+          *reinterpret_cast<uint4*>(tile + at[u] + j * (kTokens / kPieces) * 128) =
+              make_uint4(mul_f16x2(e[0], sx), mul_f16x2(e[1], sx), mul_f16x2(e[2], sx), mul_f16x2(e[3], sx));
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(tile + tile_at(row, part * 4 + u)) = out[u];
       }
+      fence_async();
     };
-    // K of the next step is on its way while V is decoded, and the other way
-    // round; page ids are a step further ahead
     int ids = page_of(0);
-    if (steps > 0) {
-      fetch(0, ids, k_codes, k_scales, kw, ks);
-      fetch(0, ids, v_codes, v_scales, vw, vs);
-    }
+    uint32_t there = request(0, ids, k_codes, k_scales, 0);
+    request(0, ids, v_codes, v_scales, L::kSlot);
     ids = page_of(1);
+    uint32_t slot = 0;  // of K of step i; V's is the next, and the one after is free
+    auto after = [](uint32_t sl) { return sl == 2 * L::kSlot ? 0u : sl + L::kSlot; };
     for (int i = 0; i < steps; ++i) {
-      const int st = i & 1, use = i >> 1;
+      const int st = i & 1;
+      const uint32_t parity = ((i >> 1) & 1) ^ 1, v_slot = after(slot), free_slot = after(v_slot);
       const int ids_after = page_of(i + 2);
-      mbar_wait(&sh, bar(kKEmpty + st), (use & 1) ^ 1);
-      write(smem + L::kK + st * L::kTile, kw, ks);
-      fence_async();
+      const uint32_t next_there = request(i + 1, ids, k_codes, k_scales, free_slot);
+      decode(slot, there, false, kKEmpty + st, parity, smem + L::kK + st * L::kTile);
       mbar_arrive(bar(kKFull + st));
-      if (i + 1 < steps) fetch(i + 1, ids, k_codes, k_scales, kw, ks);
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        // 0 * NaN would reach rows that do not see the token: NaN is taken
-        // out of the product, and the rows that see it look for it at the end
-        if ((vs[j] & 0x7Fu) == 0x7Fu) nan_v = true, vs[j] &= 0xFF00u;
-        if ((vs[j] & 0x7F00u) == 0x7F00u) nan_v = true, vs[j] &= 0x00FFu;
-      }
-      mbar_wait(&sh, bar(kVEmpty + st), (use & 1) ^ 1);
-      write(smem + L::kV + st * L::kTile, vw, vs);
-      fence_async();
+      request(i + 1, ids, v_codes, v_scales, slot);
+      decode(v_slot, there, true, kVEmpty + st, parity, smem + L::kV + st * L::kTile);
       mbar_arrive(bar(kVFull + st));
-      if (i + 1 < steps) fetch(i + 1, ids, v_codes, v_scales, vw, vs);
       ids = ids_after;
+      there = next_there;
+      slot = free_slot;
     }
     if (nan_v) *reinterpret_cast<volatile int*>(&sh.nan_v) = 1;
     mbar_arrive(bar(kScan));
@@ -522,12 +595,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int t = 0; t < 2; ++t) {
           if (t == 0) mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
           if (t == 0 && i + 1 < steps) mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
-          mbar_wait(&sh, bar(kPFull + t), i & 1);
+          const uint64_t v0 = v_desc + st * kTileStep;
+          mbar_wait(&sh, bar(kPFull + 2 * t), i & 1);
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t v0 = v_desc + st * kTileStep;
 #pragma unroll
-            for (int k = 0; k < kTokens / 16; ++k)
+            for (int k = 0; k < kTokens / 32; ++k)
+              mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, i > 0 || k > 0);
+          }
+          __syncwarp();
+          mbar_wait(&sh, bar(kPFull + 2 * t + 1), i & 1);
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = kTokens / 32; k < kTokens / 16; ++k)
               mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, i > 0 || k > 0);
             if (i + 1 < steps)
               qk(t, nst);
