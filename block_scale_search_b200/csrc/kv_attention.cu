@@ -406,8 +406,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         for (int half = 0; half < 2; ++half) {
           const uint32_t s0 = __byte_perm(ksc[half][0], 0, sel), s1 = __byte_perm(ksc[half][1], 0, sel);
           uint32_t e0[4], e1[4];
-          decode_word(kw[half][0][w], e0);
-          decode_word(kw[half][1][w], e1);
+          e2m1x8_to_f16x2(kw[half][0][w], e0);
+          e2m1x8_to_f16x2(kw[half][1][w], e1);
           const uint32_t a[4] = {mul_f16x2(e0[0], s0), mul_f16x2(e1[0], s1), mul_f16x2(e0[1], s0), mul_f16x2(e1[1], s1)};
           const uint32_t b[4] = {mul_f16x2(e0[2], s0), mul_f16x2(e1[2], s1), mul_f16x2(e0[3], s0), mul_f16x2(e1[3], s1)};
 #pragma unroll
@@ -508,10 +508,10 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         for (int w = 0; w < VW; ++w) {
           constexpr uint32_t kLow = 0x0F0F0F0Fu;
           uint32_t lo_ab[4], hi_ab[4], lo_cd[4], hi_cd[4];
-          decode_word((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), lo_ab);
-          decode_word(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), hi_ab);
-          decode_word((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), lo_cd);
-          decode_word(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), hi_cd);
+          e2m1x8_to_f16x2((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), lo_ab);
+          e2m1x8_to_f16x2(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), hi_ab);
+          e2m1x8_to_f16x2((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), lo_cd);
+          e2m1x8_to_f16x2(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), hi_cd);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint32_t a[4] = {mul_f16x2(lo_ab[u], sab), mul_f16x2(hi_ab[u], sab),

@@ -31,17 +31,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
 }
-// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
-// low half of r[i].
-__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&r)[4]) {
-  asm("{ .reg .b8 a, b, c, d;\n"
-      "mov.b32 {a, b, c, d}, %4;\n"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
-      "cvt.rn.f16x2.e2m1x2 %3, d; }"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -119,112 +119,157 @@ __device__ __forceinline__ void quantize_group(const float (&x)[16], float amax,
   }
 }
 
+// How tokens and groups of 16 (those of K, then of V) are laid over a CTA: a
+// thread keeps its group's column and takes every (grid * per_pass)-th token,
+// so that divisions are made once.  Rows with more groups than a CTA has
+// threads are taken in several rounds of columns.
+struct Columns {
+  uint32_t per_token;  // groups of a token, K and V
+  uint32_t per_pass;   // tokens a CTA takes side by side
+  int page_shift;
+};
+
+// Calls body(token, isv, head, group) for this thread's groups, kUnroll tokens
+// at a time (token < 0: nothing to do).
+template <int kUnroll, typename Body>
+__device__ __forceinline__ void for_groups(const nvfp4_kv_cache& c, const Columns& m, int64_t tokens, Body body) {
+  const uint32_t gd = c.head_dim / 16, gt = m.per_token / 2;
+  const uint32_t tl = m.per_pass > 1 ? threadIdx.x / m.per_token : 0u;
+  if (tl >= m.per_pass) return;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * m.per_pass;
+  for (uint32_t col = threadIdx.x - tl * m.per_token; col < m.per_token; col += kThreads) {
+    const bool isv = col >= gt;
+    const uint32_t r = isv ? col - gt : col, h = r / gd, g = r - h * gd;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * m.per_pass + tl; t < tokens; t += kUnroll * step) {
+      int64_t ts[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) ts[i] = t + i * step < tokens ? t + i * step : -1;
+      body(ts, isv, h, g);
+    }
+    if (m.per_pass > 1) break;
+  }
+}
+
+// Byte offsets of a group of the row at `slot` in a codes and in a scales
+// array; false for a slot that is not in the cache.
+__device__ __forceinline__ bool locate(const nvfp4_kv_cache& c, int page_shift, int64_t slot, uint32_t h, uint32_t g,
+                                       int64_t& codes, int64_t& scales) {
+  if (slot < 0 || (slot >> page_shift) >= c.num_pages) return false;
+  const uint64_t page = static_cast<uint64_t>(slot >> page_shift);
+  const uint32_t row = static_cast<uint32_t>(slot) & ((1u << page_shift) - 1);
+  const uint32_t gd = c.head_dim / 16;
+  const uint64_t in_page = (static_cast<uint64_t>(h) << page_shift) + row;
+  codes = static_cast<int64_t>(page * static_cast<uint32_t>(c.code_page_stride) + in_page * (8 * gd) + 8 * g);
+  scales = static_cast<int64_t>(page * static_cast<uint32_t>(c.scale_page_stride) + in_page * gd + g);
+  return true;
+}
+
+constexpr int kAppendUnroll = 2, kReadUnroll = 4;  // tokens whose loads are in flight per thread
+
 template <int kType>
 __global__ void __launch_bounds__(kThreads)
-kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, int64_t tokens, int tile,
+kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens,
                  const int64_t* __restrict__ slots, int* __restrict__ status) {
-  const uint32_t gd = c.head_dim / 16, gt = gd * c.kv_heads, unit = 2 * gt;
-  const int64_t page = c.page_size, nslots = c.num_pages * page;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile; t0 < tokens;
-       t0 += static_cast<int64_t>(gridDim.x) * tile) {
-    const int64_t left = tokens - t0;
-    const uint32_t n = static_cast<uint32_t>(left < tile ? left : tile) * unit;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-      const uint32_t tl = i / unit;
-      uint32_t r = i - tl * unit;
-      const bool isv = r >= gt;
-      if (isv) r -= gt;
-      const uint32_t h = r / gd, g = r - h * gd;
-      const int64_t t = t0 + tl;
-      const int64_t slot = slots[t];
-      if (slot < 0 || slot >= nslots) continue;
-      const KvRows& X = isv ? V : K;
-      const int64_t at = t * X.token_stride + h * X.head_stride + 16 * g;
-      float x[16], amax;
-      const bool finite = load_group<kType>(
-          static_cast<const char*>(X.p) + at * (kType == kFp32 ? 4 : 2), x, amax);
+  for_groups<kAppendUnroll>(c, m, tokens, [&](const int64_t(&ts)[kAppendUnroll], bool isv, uint32_t h, uint32_t g) {
+    const KvRows& X = isv ? V : K;
+    const float S = (isv ? c.v_S : c.k_S)[h];
+    uint8_t* const codes_out = isv ? c.v_codes : c.k_codes;
+    uint8_t* const scales_out = isv ? c.v_scales : c.k_scales;
+    int64_t slot[kAppendUnroll];
+    float x[kAppendUnroll][16], amax[kAppendUnroll];
+    bool finite[kAppendUnroll];
+#pragma unroll
+    for (int i = 0; i < kAppendUnroll; ++i) {
+      slot[i] = ts[i] >= 0 ? slots[ts[i]] : -1;
+      const int64_t at = (ts[i] < 0 ? 0 : ts[i]) * X.token_stride + h * X.head_stride + 16 * g;
+      finite[i] = load_group<kType>(static_cast<const char*>(X.p) + at * (kType == kFp32 ? 4 : 2), x[i], amax[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendUnroll; ++i) {
+      int64_t co, so;
+      if (!locate(c, m.page_shift, slot[i], h, g, co, so)) continue;
       uint32_t codes[2] = {0u, 0u}, scale = 0x7F;
-      if (finite)
-        quantize_group(x, amax, (isv ? c.v_S : c.k_S)[h], codes, scale);
+      if (finite[i])
+        quantize_group(x[i], amax[i], S, codes, scale);
       else if (status)
         *status = NVFP4_ERR_NONFINITE;
-      const int64_t p = slot / page, row = slot - p * page;
-      const int64_t in_page = h * page + row;
-      uint8_t* cd = (isv ? c.v_codes : c.k_codes) + p * c.code_page_stride + in_page * (gd * 8) + g * 8;
-      uint8_t* sc = (isv ? c.v_scales : c.k_scales) + p * c.scale_page_stride + in_page * gd + g;
-      *reinterpret_cast<uint2*>(cd) = make_uint2(codes[0], codes[1]);
-      *sc = static_cast<uint8_t>(scale);
+      *reinterpret_cast<uint2*>(codes_out + co) = make_uint2(codes[0], codes[1]);
+      scales_out[so] = static_cast<uint8_t>(scale);
     }
-  }
+  });
 }
 
 // -------------------------------------------------------------------- read
 
-// Value of any scale byte (0x7F and the negative codes' NaN give NaN).
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  uint32_t hh;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hh) : "h"(static_cast<uint16_t>(byte)));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(hh & 0xFFFFu)));
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 template <int kType>
 __global__ void __launch_bounds__(kThreads)
-kv_read_kernel(nvfp4_kv_cache c, int64_t tokens, int tile, const int64_t* __restrict__ slots,
-               void* __restrict__ K, void* __restrict__ V) {
-  // one thread writes half a group: 8 elements, one 16- or 32-byte store
-  const uint32_t gd = c.head_dim / 16, ht = 2 * gd * c.kv_heads, unit = 2 * ht;
-  const int64_t page = c.page_size, nslots = c.num_pages * page;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile; t0 < tokens;
-       t0 += static_cast<int64_t>(gridDim.x) * tile) {
-    const int64_t left = tokens - t0;
-    const uint32_t n = static_cast<uint32_t>(left < tile ? left : tile) * unit;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-      const uint32_t tl = i / unit;
-      uint32_t r = i - tl * unit;
-      const bool isv = r >= ht;
-      if (isv) r -= ht;
-      const uint32_t h = r / (2 * gd), e = r - h * (2 * gd);  // e: half-group of the row
-      const int64_t t = t0 + tl;
-      const int64_t slot = slots[t];
-      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (slot >= 0 && slot < nslots) {
-        const int64_t p = slot / page, row = slot - p * page;
-        const int64_t in_page = h * page + row;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-            (isv ? c.v_codes : c.k_codes) + p * c.code_page_stride + in_page * (gd * 8) + e * 4);
-        const float v = scale_value((isv ? c.v_scales : c.k_scales)[p * c.scale_page_stride + in_page * gd + e / 2]);
-        const float S = (isv ? c.v_S : c.k_S)[h];
+kv_read_kernel(nvfp4_kv_cache c, Columns m, int64_t tokens, const int64_t* __restrict__ slots, void* __restrict__ K,
+               void* __restrict__ V) {
+  constexpr int kSize = kType == kFp32 ? 4 : 2;
+  for_groups<kReadUnroll>(c, m, tokens, [&](const int64_t(&ts)[kReadUnroll], bool isv, uint32_t h, uint32_t g) {
+    const float S = (isv ? c.v_S : c.k_S)[h];
+    const uint8_t* const codes_in = isv ? c.v_codes : c.k_codes;
+    const uint8_t* const scales_in = isv ? c.v_scales : c.k_scales;
+    int64_t slot[kReadUnroll];
+    uint2 w[kReadUnroll];
+    uint32_t sc[kReadUnroll];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t hh = e2m1x2_to_f16x2((w >> (8 * j)) & 0xFFu);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-          y[2 * j] = (f.x * v) * S;  // the first product is exact (6 bits)
-          y[2 * j + 1] = (f.y * v) * S;
-        }
-      }
-      const int64_t at = (t * c.kv_heads + h) * c.head_dim + 8 * e;
-      void* out = isv ? V : K;
-      if constexpr (kType == kFp32) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(static_cast<float*>(out) + at),
-                     "r"(__float_as_uint(y[0])), "r"(__float_as_uint(y[1])), "r"(__float_as_uint(y[2])),
-                     "r"(__float_as_uint(y[3])), "r"(__float_as_uint(y[4])), "r"(__float_as_uint(y[5])),
-                     "r"(__float_as_uint(y[6])), "r"(__float_as_uint(y[7])) : "memory");
-      } else {
-        uint32_t o[4];
+    for (int i = 0; i < kReadUnroll; ++i) slot[i] = ts[i] >= 0 ? slots[ts[i]] : -1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (kType == kBf16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            const __half2 b = __floats2half2_rn(y[2 * j], y[2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < kReadUnroll; ++i) {
+      int64_t co, so;
+      w[i] = make_uint2(0u, 0u);
+      sc[i] = 0;
+      if (locate(c, m.page_shift, slot[i], h, g, co, so)) {
+        w[i] = *reinterpret_cast<const uint2*>(codes_in + co);
+        sc[i] = scales_in[so];
       }
     }
-  }
+#pragma unroll
+    for (int i = 0; i < kReadUnroll; ++i) {
+      if (ts[i] < 0) continue;
+      uint32_t hh;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hh) : "h"(static_cast<uint16_t>(sc[i] | (sc[i] << 8))));
+      char* const out = static_cast<char*>(isv ? V : K) +
+                        ((ts[i] * c.kv_heads + h) * c.head_dim + 16 * g) * kSize;
+      uint32_t r[16];
+      const uint32_t words[2] = {w[i].x, w[i].y};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t e[4];
+        e2m1x8_to_f16x2(words[u], e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // code * scale is exact in FP16 (6 bits)
+          const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&e[j]), *reinterpret_cast<const __half2*>(&hh));
+          const float2 f = __half22float2(v);
+          const float a = f.x * S, z = f.y * S;
+          if constexpr (kType == kFp32) {
+            r[8 * u + 2 * j] = __float_as_uint(a);
+            r[8 * u + 2 * j + 1] = __float_as_uint(z);
+          } else if constexpr (kType == kBf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(a, z);
+            r[4 * u + j] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            const __half2 b = __floats2half2_rn(a, z);
+            r[4 * u + j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+      }
+      const uint32_t lo[8] = {r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7]};
+      store32(out, lo);
+      if constexpr (kType == kFp32) {
+        const uint32_t hi[8] = {r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15]};
+        store32(out + 32, hi);
+      }
+    }
+  });
 }
 
 // -------------------------------------------------------------------- copy
@@ -276,19 +321,21 @@ cudaError_t copy_chunk(const nvfp4_kv_cache& c, int64_t layers, int64_t cls, int
   return cudaGetLastError();
 }
 
-// Tokens that one CTA takes at a time, and the grid: enough CTAs to fill the
-// GPU once where there are tokens for it, each with about two units a thread.
 struct TokenGrid {
-  int tile;
+  Columns m;
   unsigned blocks;
 };
-TokenGrid token_grid(int64_t tokens, int64_t units_per_token, int num_sms) {
-  int64_t tile = 2 * kThreads / units_per_token;
-  if (tile < 1) tile = 1;
-  int64_t blocks = (tokens + tile - 1) / tile;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 32;
-  if (blocks > cap) blocks = cap;
-  return {static_cast<int>(tile), static_cast<unsigned>(blocks)};
+// One wave of CTAs at most, 8 an SM.
+TokenGrid token_grid(const nvfp4_kv_cache& c, int64_t tokens, int num_sms) {
+  TokenGrid g{};
+  g.m.per_token = 2u * c.kv_heads * (c.head_dim / 16);
+  g.m.per_pass = g.m.per_token <= kThreads ? kThreads / g.m.per_token : 1;
+  while ((1 << g.m.page_shift) < c.page_size) ++g.m.page_shift;
+  int64_t blocks = (tokens + g.m.per_pass - 1) / g.m.per_pass;
+  const int64_t wave = static_cast<int64_t>(num_sms) * 8;
+  if (blocks > wave) blocks = wave;
+  g.blocks = static_cast<unsigned>(blocks);
+  return g;
 }
 
 }  // namespace
@@ -301,9 +348,9 @@ cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvR
     if (e != cudaSuccess) return e;
   }
   if (tokens == 0) return cudaSuccess;
-  const TokenGrid g = token_grid(tokens, int64_t{2} * c.kv_heads * c.head_dim / 16, num_sms);
+  const TokenGrid g = token_grid(c, tokens, num_sms);
   auto launch = [&](auto t) {
-    kv_append_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, K, V, tokens, g.tile, slots, status);
+    kv_append_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, K, V, g.m, tokens, slots, status);
   };
   if (type == kBf16) launch(std::integral_constant<int, kBf16>{});
   else if (type == kFp16) launch(std::integral_constant<int, kFp16>{});
@@ -314,9 +361,9 @@ cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvR
 cudaError_t launch_kv_read(const nvfp4_kv_cache& c, int64_t tokens, const int64_t* slots, int type,
                            void* K, void* V, int num_sms, cudaStream_t stream) {
   if (tokens == 0) return cudaSuccess;
-  const TokenGrid g = token_grid(tokens, int64_t{2} * c.kv_heads * c.head_dim / 8, num_sms);
+  const TokenGrid g = token_grid(c, tokens, num_sms);
   auto launch = [&](auto t) {
-    kv_read_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, tokens, g.tile, slots, K, V);
+    kv_read_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, g.m, tokens, slots, K, V);
   };
   if (type == kBf16) launch(std::integral_constant<int, kBf16>{});
   else if (type == kFp16) launch(std::integral_constant<int, kFp16>{});

@@ -83,11 +83,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 // Waits for a phase, for a quarter of a second at most: a wait given up is
 // counted and ends all later ones of the CTA, which then runs to its end.
+template <int kSleep>
 __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
   long long t0 = 0;
   for (uint32_t n = 1;; ++n) {
+    if constexpr (kSleep > 0) __nanosleep(kSleep);
     if (mbar_try(bar, parity)) return;
-    if ((n & 255u) != 0) continue;  // (a try suspends the thread for a while by itself)
+    if ((n & 255u) != 0) continue;
     if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
     if (t0 == 0) t0 = clock64();
     if (clock64() - t0 > (1ll << 29)) {
@@ -97,8 +99,12 @@ __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_
     }
   }
 }
+// kSleep: ns between tries; a warp that tries without a pause takes an issue
+// slot in four from the warps that work.
+constexpr int kSoftmaxSleep = 20, kDecodeSleep = 100;
+template <int kSleep = 0>
 __device__ __forceinline__ void mbar_wait(Shared* sh, uint32_t bar, uint32_t parity) {
-  if (!mbar_try(bar, parity)) mbar_wait_slow(sh, bar, parity);
+  if (!mbar_try(bar, parity)) mbar_wait_slow<kSleep>(sh, bar, parity);
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
       page = page_of(i + 1);
       const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
-      mbar_wait(&sh, bar(kSFull + t), i & 1);
+      mbar_wait<kSoftmaxSleep>(&sh, bar(kSFull + t), i & 1);
       tc_fence_after();
       uint32_t x[4][32];
 #pragma unroll
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
           if ((sc[j] & 0x7F00u) == 0x7F00u) sc[j] &= 0x00FFu;
         }
       }
-      mbar_wait(&sh, bar(bar_empty), parity);
+      mbar_wait<kDecodeSleep>(&sh, bar(bar_empty), parity);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const uint32_t two = e4m3x2_to_f16x2(sc[j]);
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t e[4];
-          decode_word(wv[u], e);
+          e2m1x8_to_f16x2(wv[u], e);
           const uint32_t sx = u < 2 ? s0 : s1;
           *reinterpret_cast<uint4*>(tile + at[u] + j * (kTokens / kPieces) * 128) =
               make_uint4(mul_f16x2(e[0], sx), mul_f16x2(e[1], sx), mul_f16x2(e[2], sx), mul_f16x2(e[3], sx));
