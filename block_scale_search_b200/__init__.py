@@ -177,6 +177,8 @@ _SIGS = {
 def lib(path: str | None = None):
     """Load the shared library (built in-tree by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             # NVFP4HS_LIB selects another build of the library, e.g. the
@@ -884,29 +886,34 @@ class KVCache:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_S, self.v_S = k_S, v_S
         shape, small = k_codes.shape, k_scales.shape
-        dims = len(shape)
-        if dims not in (4, 5):
+        if len(shape) not in (4, 5):
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim/2], or that after layers")
-        lead, dim = shape[:-1], 2 * shape[-1]
-        if small[:-1] != lead or 16 * small[-1] != dim or v_codes.shape != shape or v_scales.shape != small:
+        pages, h, p, half = shape[-4:]
+        dim = 2 * half
+        if small[:-1] != shape[:-1] or 16 * small[-1] != dim or v_codes.shape != shape or v_scales.shape != small:
             raise ValueError("codes and scales of K and V must agree in shape")
         stride, small_stride = k_codes.stride(), k_scales.stride()
         if v_codes.stride() != stride or v_scales.stride() != small_stride:
             raise ValueError("K and V must have the same strides")
-        h, p = shape[-3], shape[-2]
-        if stride[-3:] != (p * dim // 2, dim // 2, 1) or small_stride[-3:] != (p * dim // 16, dim // 16, 1):
+        if stride[-3:] != (p * half, half, 1) or small_stride[-3:] != (p * dim // 16, dim // 16, 1):
             raise ValueError("a page must be contiguous")
-        self.layers = shape[0] if dims == 5 else 1
-        s_shape = (self.layers, h) if dims == 5 else (h,)
+        s_shape = (h,)
+        self.layers = 1
+        if len(shape) == 5:
+            self.layers = shape[0]
+            s_shape = (shape[0], h)
         self.device = k_codes.device
-        for t, kind in ((k_codes, torch.uint8), (k_scales, torch.uint8), (v_codes, torch.uint8),
-                        (v_scales, torch.uint8), (k_S, torch.float32), (v_S, torch.float32)):
-            if t.dtype != kind or t.device != self.device or not t.is_cuda:
-                raise ValueError("codes and scales must be uint8, S float32, on one CUDA device")
+        where = k_codes.get_device()  # -1 on the CPU
+        u8, f32 = torch.uint8, torch.float32
+        if (where < 0 or k_codes.dtype is not u8 or k_scales.dtype is not u8 or v_codes.dtype is not u8
+                or v_scales.dtype is not u8 or k_S.dtype is not f32 or v_S.dtype is not f32
+                or k_scales.get_device() != where or v_codes.get_device() != where
+                or v_scales.get_device() != where or k_S.get_device() != where or v_S.get_device() != where):
+            raise ValueError("codes and scales must be uint8, S float32, on one CUDA device")
         if k_S.shape != s_shape or v_S.shape != s_shape or not k_S.is_contiguous() or not v_S.is_contiguous():
             raise ValueError("S must be contiguous [kv_heads], or [layers, kv_heads]")
         self.desc = KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), shape[-4],
+                                v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), pages,
                                 stride[-4], small_stride[-4], p, h, dim)
 
     @classmethod
@@ -950,34 +957,24 @@ def _kv_rows(t, name, heads, dim, device, types):
 
 
 def _int_vector(t, name, kind, device, n=None):
-    if t.dtype != kind or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+    if t.dtype is not kind or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{name} must be a contiguous {kind} vector" + (f" of {n}" if n is not None else "") +
                          " on the cache's device")
     return t
 
 
-class _On:
-    """Makes a device current for a call, and a given stream current for what
-    the call allocates (so that the allocator knows where it is used)."""
-
-    __slots__ = ("ctx",)
-
-    def __init__(self, device, stream):
-        self.ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _on(call, device, stream):
+    """call() with the device current, and with a given stream current for what
+    it allocates (so that the allocator knows where that is used)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(device):
+        if stream is None:
+            return call()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return call()
 
 
 def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
@@ -995,9 +992,8 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
     _int_vector(slots, "slots", torch.int64, cache.device, n)
     if status is not None:
         _int_vector(status, "status", torch.int32, cache.device, 1)
-    with _On(cache.device, stream):
-        nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, K.stride(0), K.stride(1), V.stride(0), V.stride(1),
-                        slots, status)
+    _on(lambda: nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, K.stride(0), K.stride(1), V.stride(0), V.stride(1),
+                                slots, status), cache.device, stream)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, out=None, stream=None):
@@ -1008,28 +1004,34 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
     if dtype not in _TYPES:
         raise ValueError("dtype must be bfloat16, float16 or float32")
     n = slots.numel()
-    with _On(cache.device, stream):
-        if out is None:
-            K, V = (torch.empty(n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device) for _ in range(2))
+    if out is not None:
+        K, V = (_kv_rows(t, "out", d.kv_heads, d.head_dim, cache.device, (dtype,)) for t in out)
+        if not (K.is_contiguous() and V.is_contiguous() and K.shape[0] == V.shape[0] == n):
+            raise ValueError("out must be two contiguous tensors with a row for every slot")
+
+    def call():
+        if out is not None:
+            k, v = out
         else:
-            K, V = (_kv_rows(t, "out", d.kv_heads, d.head_dim, cache.device, (dtype,)) for t in out)
-            if not (K.is_contiguous() and V.is_contiguous() and K.shape[0] == V.shape[0] == n):
-                raise ValueError("out must be two contiguous tensors with a row for every slot")
-        nvfp4_kv_read(d, slots, n, _TYPES[dtype], K, V)
-    return K, V
+            k, v = torch.empty(2, n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device).unbind(0)
+        nvfp4_kv_read(d, slots, n, _TYPES[dtype], k, v)
+        return k, v
+
+    return _on(call, cache.device, stream)
 
 
 def kv_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     """Page dst[i] becomes page src[i] in every layer of the cache.  src, dst: page
     ids on the host (int32 CPU tensors or sequences); no page may be written
     twice, or both read and written."""
-    src, dst = (torch.as_tensor(t, dtype=torch.int32, device="cpu").contiguous() for t in (src, dst))
+    src, dst = (t if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cpu and t.is_contiguous()
+                else torch.as_tensor(t, dtype=torch.int32, device="cpu").contiguous() for t in (src, dst))
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be lists of as many pages")
     many = cache.k_codes.dim() == 5
-    with _On(cache.device, stream):
-        nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
-                            cache.k_scales.stride(0) if many else 0, src, dst, src.numel())
+    _on(lambda: nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
+                                    cache.k_scales.stride(0) if many else 0, src, dst, src.numel()),
+        cache.device, stream)
 
 
 def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_lengths: torch.Tensor,
@@ -1057,28 +1059,27 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
         raise ValueError("page_table must be int32 [batch, pages], rows contiguous, on the cache's device")
     if max_kv > page_table.shape[1] * d.page_size:
         raise ValueError("max_kv is more than the page table's rows hold")
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty(total, heads, d.head_dim, dtype=Q.dtype, device=dev)
-        else:
-            _kv_rows(out, "out", heads, d.head_dim, dev, (Q.dtype,))
-            if out.shape[0] != total:
-                raise ValueError("out must have Q's rows")
-        if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (total, heads) or lse.device != dev or not lse.is_contiguous():
-                raise ValueError("lse must be contiguous float32 [total, q_heads]")
-        elif want_lse:
-            lse = torch.empty(total, heads, dtype=torch.float32, device=dev)
-        if batch and total and max_q > 0:
+    if out is not None:
+        _kv_rows(out, "out", heads, d.head_dim, dev, (Q.dtype,))
+        if out.shape[0] != total:
+            raise ValueError("out must have Q's rows")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads) or lse.device != dev
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [total, q_heads]")
+
+    def call():
+        o = torch.empty_like(Q) if out is None else out
+        z = torch.empty(total, heads, dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        ws = workspace
+        if ws is None and batch and total and max_q > 0:
             nb = nvfp4_kv_attention_workspace_size(batch, max_q, max_kv, heads, d.kv_heads, d.head_dim)
             if nb == 0:
                 raise NVFP4Error("nvfp4_kv_attention_workspace_size", -1)
-            if workspace is None:
-                workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
-        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, Q.stride(0), Q.stride(1), q_offsets,
-                           kv_lengths, page_table, max(page_table.stride(0), page_table.shape[1]),
-                           batch, max_q, max_kv,
-                           d.head_dim ** -0.5 if sm_scale is None else sm_scale, causal, window, out,
-                           out.stride(0), out.stride(1), lse, workspace,
-                           workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    return (out, lse) if lse is not None else out
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, Q.stride(0), Q.stride(1), q_offsets, kv_lengths,
+                           page_table, max(page_table.stride(0), page_table.shape[1]), batch, max_q, max_kv,
+                           d.head_dim ** -0.5 if sm_scale is None else sm_scale, causal, window, o, o.stride(0),
+                           o.stride(1), z, ws, ws.numel() * ws.element_size() if ws is not None else 0)
+        return o if z is None else (o, z)
+
+    return _on(call, dev, stream)

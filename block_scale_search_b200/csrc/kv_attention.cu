@@ -135,10 +135,10 @@ __device__ __forceinline__ long long units_before(const Params& p, int n, long l
   return v;
 }
 
-// Units per CTA: an equal share, but no less than an item of a tile a warp.
+// Units per CTA: an equal share, but no less than a tile a warp.
 __device__ __forceinline__ long long units_per_cta(long long total, int ctas) {
   const long long share = (total + ctas - 1) / ctas;
-  return share > kWarps + kItemCost ? share : kWarps + kItemCost;
+  return share > kWarps ? share : kWarps;
 }
 
 template <int D, int NT>
@@ -163,6 +163,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   constexpr int kRing = ring_bytes(D);
   uint4* const q = reinterpret_cast<uint4*>(smem + kRing) + warp * NT * KW * 32 + lane;
   const uint32_t ring_u = smem_u32(ring);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // kv_join_kernel may be set up meanwhile
 
   // this CTA's piece of the line of work
   const long long total = units_before<R>(p, p.a.batch, red);
@@ -612,12 +614,16 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   const Seq s = sequence<R>(p, b);
   const int row = blockIdx.x % R, item = blockIdx.x / R;
   const int h = item % p.a.c.kv_heads, rb = item / p.a.c.kv_heads;
-  if (rb >= s.blocks || rb * R + row >= s.lq * p.group) return;
+  // Every CTA waits for kv_rows_kernel before it ends, also where it has
+  // nothing to add up: what follows on the stream waits for this kernel only.
+  auto rows_done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+  if (rb >= s.blocks || rb * R + row >= s.lq * p.group) return rows_done();
   const long long base = units_before<R>(p, b, red);
   const long long total = units_before<R>(p, p.a.batch, red);
   const long long per = units_per_cta(total, p.ctas);
   const long long first = base + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
   const long long c0 = first / per, c1 = last / per;
+  rows_done();
   if (c0 == c1) return;
   auto at = [&](long long cta) {
     const int slot = cta * per <= first ? 1 : 0;
@@ -696,7 +702,7 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   const double tiles = static_cast<double>(batch) * kv_heads * static_cast<double>((p.rows + 8 * p.nt - 1) / (8 * p.nt)) *
                        static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
   const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(p.nt);
-  const double want = tiles / (kWarps + kItemCost) + 1.0;
+  const double want = tiles / kWarps + 1.0;
   p.ctas = static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
   return p;
 }
@@ -705,17 +711,25 @@ template <int D, int NT>
 cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
   constexpr int R = 8 * NT;
   constexpr int smem = rows_smem(D, NT);
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_rows_kernel<D, NT>),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.set(reinterpret_cast<const void*>(&kv_rows_kernel<D, NT>), smem);
   if (e != cudaSuccess) return e;
   p.partial_ml = p.partial + static_cast<int64_t>(p.ctas) * 2 * R * D;
   kv_rows_kernel<D, NT><<<p.ctas, kThreads, smem, stream>>>(p);
-  cudaError_t r = cudaGetLastError();
-  if (r != cudaSuccess) return r;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the joining kernel is launched while the first still runs (programmatic
+  // dependent launch) and waits for its end on the device
   const int blocks = static_cast<int>((plan.rows + R - 1) / R);
-  const dim3 grid(static_cast<unsigned>(blocks) * p.a.c.kv_heads * R, static_cast<unsigned>(p.a.batch));
-  kv_join_kernel<D, NT><<<grid, kThreads, 0, stream>>>(p, blocks);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks) * p.a.c.kv_heads * R, static_cast<unsigned>(p.a.batch));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, static_cast<const Params&>(p), blocks);
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // a call's parameters, number conversions, the mask, and the results' rounding.
 #pragma once
 
+#include <atomic>
+
 #include "kv_cache.cuh"
 #include "nvfp4_device.cuh"
 
@@ -18,6 +20,21 @@ struct Params {
   int ctas;
   int rows_limit;  // kv_rows_kernel serves sequences with at most so many query rows for a KV head
   int row_blocks;  // of kv_prompt_kernel
+};
+
+// Raises a kernel's limit of dynamic shared memory, once per device.
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};  // bit d: set on device d
+  cudaError_t set(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
 };
 
 // Prompts (kv_prompt.cu).

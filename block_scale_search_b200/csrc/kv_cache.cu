@@ -82,29 +82,72 @@ __device__ __noinline__ uint32_t e2m1_exact(float a, float v, float S) {
   return k;
 }
 
+// Eight floats to E2M1 nibbles, round-to-nearest-even, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x8_rne(f32x2_t a, f32x2_t b, f32x2_t c, f32x2_t d) {
+  float f[8];
+  f2_unpack(a, f[0], f[1]);
+  f2_unpack(b, f[2], f[3]);
+  f2_unpack(c, f[4], f[5]);
+  f2_unpack(d, f[6], f[7]);
+  uint32_t r;
+  asm("{ .reg .b8 p, q, r, s;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n"
+      "mov.b32 %0, {p, q, r, s}; }"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+
+// A head's S, 1 / (6 S), and whether S is far enough from the ends of the FP32
+// range for products with that to be within rounding of the quotients.
+struct HeadScale {
+  float S, inv6;
+  bool plain;
+};
+__device__ __forceinline__ HeadScale head_scale(float S) {
+  return {S, __fdividef(1.0f, 6.0f * S), S > 0x1p-100f && S < 0x1p100f};
+}
+
 // Codes of one group (element i in nibble i) and its scale byte.  A zero
 // magnitude is stored without a sign.
-__device__ __forceinline__ void quantize_group(const float (&x)[16], float amax, float S,
+__device__ __forceinline__ void quantize_group(const float (&x)[16], float amax, const HeadScale& hs,
                                                uint32_t (&codes)[2], uint32_t& scale) {
-  const int b = amax == 0.0f ? 0 : clamp_code(e4m3_code_rne_sat(__fdiv_rn(__fdiv_rn(amax, 6.0f), S)));
+  const float S = hs.S;
+  // The scale code of fl32(fl32(a / 6) / S): as below, from a quotient taken
+  // too small and too large; the divisions themselves where the two differ.
+  const float u = amax * hs.inv6;
+  uint32_t two;
+  asm("{ .reg .b16 t; cvt.rn.satfinite.e4m3x2.f32 t, %1, %2; cvt.u32.u16 %0, t; }"
+      : "=r"(two) : "f"(u * (1.0f + 0x1p-20f)), "f"(u * (1.0f - 0x1p-20f)));
+  int b = two & 0xFF;
+  if (b != static_cast<int>(two >> 8) || !hs.plain || !(u > 0x1p-100f && u < 0x1p100f))
+    b = e4m3_code_rne_sat(__fdiv_rn(__fdiv_rn(amax, 6.0f), S));
+  b = amax == 0.0f ? 0 : clamp_code(b);
   scale = b;
   codes[0] = codes[1] = 0;
   if (b == 0) return;
   const float v = e4m3_value(b);
   const float vs = v * S;
-  // Fast path: y = x / (v S) within 2^-21, rounded by the hardware's E2M1
-  // conversion.  Its decision is the exact one unless y lies within 2^-20 of a
-  // midpoint; every midpoint is a float whose low 21 bits are 0, so the test
-  // is on those bits (it also sends 0 and grid values to the exact path).
-  uint32_t near = 0xFFFFFFFFu;
+  // Fast path: the hardware's E2M1 conversion of x / (v S) taken a little too
+  // small and a little too large (by 2^-20 to 2^-19; the reciprocal and the
+  // products are within 2^-21).  Rounding is monotone, so where both give the
+  // same codes they are those of the exact quotient; otherwise some element is
+  // next to a midpoint, and the group's decisions are taken exactly.
   const float inv = __fdividef(1.0f, vs);
+  const f32x2_t lo = f2_pack(inv * (1.0f - 0x1.8p-20f), inv * (1.0f - 0x1.8p-20f));
+  const f32x2_t hi = f2_pack(inv * (1.0f + 0x1.8p-20f), inv * (1.0f + 0x1.8p-20f));
+  uint32_t other[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y0 = x[2 * i] * inv, y1 = x[2 * i + 1] * inv;
-    near = min(near, min((__float_as_uint(y0) + 8u) & 0x1FFFFFu, (__float_as_uint(y1) + 8u) & 0x1FFFFFu));
-    codes[i >> 2] |= e2m1x2_rne(y0, y1) << (8 * (i & 3));
+  for (int i = 0; i < 2; ++i) {
+    codes[i] = e2m1x8_rne(f2_mul(f2_pack(x[8 * i], x[8 * i + 1]), lo), f2_mul(f2_pack(x[8 * i + 2], x[8 * i + 3]), lo),
+                          f2_mul(f2_pack(x[8 * i + 4], x[8 * i + 5]), lo), f2_mul(f2_pack(x[8 * i + 6], x[8 * i + 7]), lo));
+    other[i] = e2m1x8_rne(f2_mul(f2_pack(x[8 * i], x[8 * i + 1]), hi), f2_mul(f2_pack(x[8 * i + 2], x[8 * i + 3]), hi),
+                          f2_mul(f2_pack(x[8 * i + 4], x[8 * i + 5]), hi), f2_mul(f2_pack(x[8 * i + 6], x[8 * i + 7]), hi));
   }
-  if (near <= 16u || !(vs > 0x1p-100f && vs < 0x1p100f)) {
+  if (codes[0] != other[0] || codes[1] != other[1] || !(vs > 0x1p-100f && vs < 0x1p100f)) {
     codes[0] = codes[1] = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -167,12 +210,12 @@ __device__ __forceinline__ bool locate(const nvfp4_kv_cache& c, int page_shift, 
 constexpr int kAppendUnroll = 2, kReadUnroll = 4;  // tokens whose loads are in flight per thread
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens,
                  const int64_t* __restrict__ slots, int* __restrict__ status) {
   for_groups<kAppendUnroll>(c, m, tokens, [&](const int64_t(&ts)[kAppendUnroll], bool isv, uint32_t h, uint32_t g) {
     const KvRows& X = isv ? V : K;
-    const float S = (isv ? c.v_S : c.k_S)[h];
+    const HeadScale S = head_scale((isv ? c.v_S : c.k_S)[h]);
     uint8_t* const codes_out = isv ? c.v_codes : c.k_codes;
     uint8_t* const scales_out = isv ? c.v_scales : c.k_scales;
     int64_t slot[kAppendUnroll];

@@ -642,8 +642,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
 template <int D>
 cudaError_t run_prompt(const Params& p, cudaStream_t stream) {
   constexpr int smem = Layout<D>::kBytes + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_prompt_kernel<D>),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(&kv_prompt_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
