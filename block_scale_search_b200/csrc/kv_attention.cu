@@ -56,12 +56,12 @@ constexpr int64_t kRowsLimit = 32;
 // Resident CTAs the kernel is built for (its registers and shared memory).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : (nt == 2 ? 4 : 2); }
 
-// Shared memory: the rings [warp][stage] and the queries' operands [warp][8-row
+// Shared memory: the rings [warp][stage] and the queries' operands [8-row
 // tile][word][lane] of 16 bytes; once an item's tiles are used up, the join
 // area, sums [warp][R][D] and maxima and sums [warp][R][2], lies over both.
 __host__ __device__ constexpr int ring_bytes(int D) { return kWarps * kStages * 2 * kTile * (D / 2 + D / 16); }
 __host__ __device__ constexpr int rows_smem(int D, int NT) {
-  const int use = ring_bytes(D) + kWarps * NT * (D / 32) * 512, join = kWarps * 8 * NT * (D + 2) * 4;
+  const int use = ring_bytes(D) + NT * (D / 32) * 512, join = kWarps * 8 * NT * (D + 2) * 4;
   return use > join ? use : join;
 }
 
@@ -119,27 +119,57 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-
-// Sum of seq_units over b < n, by the whole CTA (every thread gets it).
-template <int R>
-__device__ __forceinline__ long long units_before(const Params& p, int n, long long* red) {
-  long long v = 0;
-  for (int b = threadIdx.x; b < n; b += kThreads) v += seq_units<R>(p, b);
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += red[w];
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += up;
+  }
   return v;
+}
+
+// Sums of seq_units over b < n1 (x) and b < n2 (y), n1 <= n2, by the whole CTA
+// (every thread gets them).  red: 2 kWarps.
+template <int R>
+__device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n2, long long* red) {
+  long long x = 0, y = 0;
+  for (int b = threadIdx.x; b < n2; b += kThreads) {
+    const long long n = seq_units<R>(p, b);
+    y += n;
+    if (b < n1) x += n;
+  }
+  x = warp_sum(x);
+  y = warp_sum(y);
+  if ((threadIdx.x & 31) == 0) {
+    red[threadIdx.x >> 5] = x;
+    red[kWarps + (threadIdx.x >> 5)] = y;
+  }
+  __syncthreads();
+  longlong2 r = {0, 0};
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    r.x += red[w];
+    r.y += red[kWarps + w];
+  }
+  return r;
+}
+
+// a / b for b > 0, a >= 0; the 64-bit division is long and hardly ever needed
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return (a >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
 // Units per CTA: an equal share, but no less than a tile a warp.
 __device__ __forceinline__ long long units_per_cta(long long total, int ctas) {
-  const long long share = (total + ctas - 1) / ctas;
+  const long long share = quotient(total + ctas - 1, ctas);
   return share > kWarps ? share : kWarps;
 }
+
+// Of a query row of the item: factor of its scores (base 2), visible tokens.
+struct RowInfo {
+  float f;
+  int lo, hi;
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
@@ -153,7 +183,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join_o = reinterpret_cast<float*>(smem);
   float* const join_ml = join_o + kWarps * R * D;
-  __shared__ long long red[kWarps];
+  __shared__ long long red[2 * kWarps];
+  __shared__ RowInfo row_info[R];
 
   // from lane 0, so that the compiler takes it, and branches on it, as uniform
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -161,32 +192,50 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   const nvfp4_kv_cache& c = p.a.c;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
   constexpr int kRing = ring_bytes(D);
-  uint4* const q = reinterpret_cast<uint4*>(smem + kRing) + warp * NT * KW * 32 + lane;
+  uint4* const q_all = reinterpret_cast<uint4*>(smem + kRing);
+  const uint4* const q = q_all + lane;
   const uint32_t ring_u = smem_u32(ring);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // kv_join_kernel may be set up meanwhile
 
-  // this CTA's piece of the line of work
-  const long long total = units_before<R>(p, p.a.batch, red);
-  const long long per = units_per_cta(total, p.ctas);
-  long long cur = per * blockIdx.x;
-  const long long end = min(total, cur + per);
-  if (cur >= end) return;
-  // the sequence that holds unit `cur`
+  // this CTA's piece of the line of work, and the sequence that holds its start
+  __shared__ int start_b;
+  __shared__ long long start_base;
   int b = 0;
-  long long base = 0;
-  {
-    // every warp scans 32 sequences at a time
-    for (;; b += 32) {
+  long long base = 0, cur, end;  // base: first unit of sequence b
+  if (p.a.batch <= kThreads) {   // a sequence a thread: one look at the lengths
+    const long long n = threadIdx.x < p.a.batch ? seq_units<R>(p, threadIdx.x) : 0;
+    long long inc = warp_scan(n, lane);
+    if (lane == 31) red[warp] = inc;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) inc += red[w];
+      total += red[w];
+    }
+    const long long per = units_per_cta(total, p.ctas);
+    cur = per * blockIdx.x;
+    end = min(total, cur + per);
+    if (inc - n <= cur && cur < inc) {
+      start_b = threadIdx.x;
+      start_base = inc - n;
+    }
+    __syncthreads();
+    if (cur >= end) return;
+    b = start_b;
+    base = start_base;
+  } else {
+    const long long total = units_before<R>(p, p.a.batch, p.a.batch, red).y;
+    const long long per = units_per_cta(total, p.ctas);
+    cur = per * blockIdx.x;
+    end = min(total, cur + per);
+    if (cur >= end) return;
+    for (;; b += 32) {  // every warp scans 32 sequences at a time
       if (b >= p.a.batch) return;
       const int bb = b + lane;
       const long long n = bb < p.a.batch ? seq_units<R>(p, bb) : 0;
-      long long inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += up;
-      }
+      const long long inc = warp_scan(n, lane);
       const unsigned past = __ballot_sync(0xFFFFFFFFu, base + inc > cur);
       if (past) {
         const int f = __ffs(past) - 1;
@@ -201,7 +250,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   while (cur < end) {
     const Seq s = sequence<R>(p, b);
     const long long in_seq = cur - base;
-    const int item = static_cast<int>(in_seq / s.span);
+    const int item = static_cast<int>(quotient(in_seq, s.span));
     const int us = static_cast<int>(in_seq - static_cast<long long>(item) * s.span);
     const int ue = static_cast<int>(min(static_cast<long long>(s.span), us + (end - cur)));
     const int ts = max(0, us - kItemCost), te = max(0, ue - kItemCost);  // this CTA's tiles of the item
@@ -227,16 +276,34 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2);
     const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16);
     const int* const row_table = p.a.table + b * p.a.table_stride;
-    auto page_at = [&](int k, int half) {  // page id of half a tile, or -1
+    auto page_at = [&](int k, int half) {  // the table's entry for half a tile, or -1
       const int tok = (s.t0 + ts + warp + k * kWarps) * kTile + half * kHalf;
       if (k >= mine || tok >= s.lk) return -1;
-      const int id = row_table[tok >> p.page_shift];
-      return id >= 0 && id < c.num_pages ? id : -1;
+      return row_table[tok >> p.page_shift];  // (looked at when it is used: a look waits for the load)
     };
     // lane i: pages of tile ids_base + i
     int ids0 = page_at(lane, 0), ids1 = page_at(lane, 1), ids_base = 0;
     uint32_t dead = 0;  // bits 2 (tile % 16), + 1: no page there (zeros are written)
     int requested = 0;
+    // The queries' loads go out before the tiles': behind them they would wait
+    // for the whole GPU's first requests to be served.  A thread takes 8
+    // elements (piece `qp` of a row) of NT rows.
+    constexpr int kRowPieces = D / 8, kPass = kThreads / kRowPieces;  // rows of a pass
+    const int qp = threadIdx.x % kRowPieces, qr = threadIdx.x / kRowPieces;
+    constexpr int kPasses = (R + kPass - 1) / kPass;
+    uint4 qv[kPasses];
+#pragma unroll
+    for (int n = 0; n < kPasses; ++n) {
+      const int row = r0 + qr + n * kPass;
+      qv[n] = make_uint4(0u, 0u, 0u, 0u);
+      if (qr + n * kPass < R && row < s.lq * p.group) {
+        const int qi = row / p.group, gi = row - qi * p.group;
+        qv[n] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.Q) + (s.q0 + qi) * p.a.q_token_stride +
+                                                (h * p.group + gi) * p.a.q_head_stride + 8 * qp);
+      }
+    }
+    const float kS = c.k_S[h];
+
     // scale bytes: lanes 8 i .. 8 i + 7 (D = 64: 4 i .. 4 i + 3) copy those of
     // K (i < 2) or V of half i % 2
     constexpr int kScaleLanes = kScales / 16;
@@ -261,13 +328,14 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         }
         const int id0 = __shfl_sync(0xFFFFFFFFu, ids0, requested - ids_base);
         const int id1 = __shfl_sync(0xFFFFFFFFu, ids1, requested - ids_base);
-        const uint32_t none = (id0 < 0 ? 1u : 0u) | (id1 < 0 ? 2u : 0u);
+        const bool ok0 = id0 >= 0 && id0 < c.num_pages, ok1 = id1 >= 0 && id1 < c.num_pages;
+        const uint32_t none = (ok0 ? 0u : 1u) | (ok1 ? 0u : 2u);
         const int sh = 2 * (requested & 15);
         dead = (dead & ~(3u << sh)) | (none << sh);
         const uint32_t row0 = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
         const uint32_t row1 = (row0 + kHalf) & (c.page_size - 1);
-        const int n0 = id0 < 0 ? 0 : 16, n1 = id1 < 0 ? 0 : 16;
-        const uint32_t p0 = max(id0, 0), p1 = max(id1, 0);
+        const int n0 = ok0 ? 16 : 0, n1 = ok1 ? 16 : 0;
+        const uint32_t p0 = ok0 ? id0 : 0, p1 = ok1 ? id1 : 0;
         const uint64_t off0 = static_cast<uint64_t>(p0) * code_page + row0 * (D / 2);
         const uint64_t off1 = static_cast<uint64_t>(p1) * code_page + row1 * (D / 2);
         const uint32_t dst = code_dst + fill;
@@ -294,64 +362,51 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) request();
 
-    // ---- query rows: lane (g, l4) holds d [l4 D/4, (l4+1) D/4) of row g of
-    // every 8-row tile, in FP16 after scaling the row's maximum to [1, 2)
+    // ---- query rows in FP16, a row's maximum scaled to [1, 2), as the lanes
+    // of every warp will read them: lane (g, l4) has d [l4 D/4, (l4+1) D/4) of
+    // row g of an 8-row tile, word w of it at [tile][w][lane]
+#pragma unroll
+    for (int n = 0; n < kPasses; ++n) {
+      const int r = qr + n * kPass;
+      const uint32_t w[4] = {qv[n].x, qv[n].y, qv[n].z, qv[n].w};
+      float y[8], mx = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = to_f32(w[j] & 0xFFFFu, p.a.type);
+        y[2 * j + 1] = to_f32(w[j] >> 16, p.a.type);
+        mx = fmaxf(mx, fmaxf(fabsf(y[2 * j]), fabsf(y[2 * j + 1])));
+      }
+#pragma unroll
+      for (int off = 1; off < kRowPieces; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+      float shrink, fs;
+      row_scale(mx, p.scale_log2 * kS, shrink, fs);
+      if (r < R) {
+        q_all[((r >> 3) * KW + qp % KW) * 32 + (r & 7) * 4 + qp / KW] =
+            make_uint4(pack_f16x2(y[0] * shrink, y[1] * shrink), pack_f16x2(y[2] * shrink, y[3] * shrink),
+                       pack_f16x2(y[4] * shrink, y[5] * shrink), pack_f16x2(y[6] * shrink, y[7] * shrink));
+        if (qp == 0) {
+          RowInfo info;
+          info.f = fs;
+          visible(p, s, r0 + r, info.lo, info.hi);
+          row_info[r] = info;
+        }
+      }
+    }
+    __syncthreads();
     float f[NT][2];              // factor of the scores of columns 2 l4, 2 l4 + 1
     int vlo[NT][2], vhi[NT][2];  // visible tokens of those columns
-    int all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row sees
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = r0 + 8 * n + g;
-      const bool have = row < s.lq * p.group;
-      float y[KW * 8];
-      float mx = 0.0f;
-      if (have) {
-        const uint16_t* src = static_cast<const uint16_t*>(p.a.Q) +
-                              (s.q0 + row / p.group) * p.a.q_token_stride +
-                              (h * p.group + row % p.group) * p.a.q_head_stride + l4 * (D / 4);
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[8 * i + 2 * j] = to_f32(w[j] & 0xFFFFu, p.a.type);
-            y[8 * i + 2 * j + 1] = to_f32(w[j] >> 16, p.a.type);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < KW * 8; ++i) y[i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < KW * 8; ++i) mx = fmaxf(mx, fabsf(y[i]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      float shrink, fs;
-      row_scale(mx, p.scale_log2 * c.k_S[h], shrink, fs);
-#pragma unroll
-      for (int w = 0; w < KW; ++w)
-        q[(n * KW + w) * 32] = make_uint4(pack_f16x2(y[8 * w] * shrink, y[8 * w + 1] * shrink),
-                                          pack_f16x2(y[8 * w + 2] * shrink, y[8 * w + 3] * shrink),
-                                          pack_f16x2(y[8 * w + 4] * shrink, y[8 * w + 5] * shrink),
-                                          pack_f16x2(y[8 * w + 6] * shrink, y[8 * w + 7] * shrink));
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        f[n][k] = __shfl_sync(0xFFFFFFFFu, fs, (2 * l4 + k) * 4);
-        visible(p, s, r0 + 8 * n + 2 * l4 + k, vlo[n][k], vhi[n][k]);
-        if (r0 + 8 * n + 2 * l4 + k < s.lq * p.group) {
-          all_lo = max(all_lo, vlo[n][k]);
-          all_hi = min(all_hi, vhi[n][k]);
-        }
+        const RowInfo info = row_info[8 * n + 2 * l4 + k];
+        f[n][k] = info.f;
+        vlo[n][k] = info.lo;
+        vhi[n][k] = info.hi;
       }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      all_lo = max(all_lo, __shfl_xor_sync(0xFFFFFFFFu, all_lo, o));
-      all_hi = min(all_hi, __shfl_xor_sync(0xFFFFFFFFu, all_hi, o));
-    }
-    all_lo = __shfl_sync(0xFFFFFFFFu, all_lo, 0);
-    all_hi = __shfl_sync(0xFFFFFFFFu, all_hi, 0);
+    // tokens that every row sees: a row's bounds grow with its position
+    const int all_lo = __shfl_sync(0xFFFFFFFFu, row_info[min(R, s.lq * p.group - r0) - 1].lo, 0);
+    const int all_hi = __shfl_sync(0xFFFFFFFFu, row_info[0].hi, 0);
 
     float o[NT][VW * 4][4] = {};
     // running maximum (base-2 exponent), what to add to a score for it (0 while
@@ -609,7 +664,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ Params p, int blocks) {
   constexpr int R = 8 * NT;
-  __shared__ long long red[kWarps];
+  __shared__ long long red[2 * kWarps];
   const int b = blockIdx.y;
   const Seq s = sequence<R>(p, b);
   const int row = blockIdx.x % R, item = blockIdx.x / R;
@@ -618,8 +673,8 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   // nothing to add up: what follows on the stream waits for this kernel only.
   auto rows_done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   if (rb >= s.blocks || rb * R + row >= s.lq * p.group) return rows_done();
-  const long long base = units_before<R>(p, b, red);
-  const long long total = units_before<R>(p, p.a.batch, red);
+  const longlong2 units = units_before<R>(p, b, p.a.batch, red);
+  const long long base = units.x, total = units.y;
   const long long per = units_per_cta(total, p.ctas);
   const long long first = base + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
   const long long c0 = first / per, c1 = last / per;
