@@ -49,7 +49,7 @@ constexpr int kHalf = kTile / 2;
 constexpr int kStages = 2;   // tiles of a warp's ring
 // What starting and finishing an item costs a CTA, in tiles: its page ids and
 // queries arrive in two trips to memory, its warps meet twice at the end.
-constexpr int kItemCost = 8;
+constexpr int kItemCost = 10;
 // Query rows of a sequence and KV head up to which this kernel serves it.
 constexpr int64_t kRowsLimit = 32;
 
@@ -129,11 +129,12 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane) {  // incl
 }
 
 // Sums of seq_units over b < n1 (x) and b < n2 (y), n1 <= n2, by the whole CTA
-// (every thread gets them).  red: 2 kWarps.
-template <int R>
+// of kW warps (every thread
+// gets them).  red: 2 kW.
+template <int R, int kW>
 __device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n2, long long* red) {
   long long x = 0, y = 0;
-  for (int b = threadIdx.x; b < n2; b += kThreads) {
+  for (int b = threadIdx.x; b < n2; b += 32 * kW) {
     const long long n = seq_units<R>(p, b);
     y += n;
     if (b < n1) x += n;
@@ -142,14 +143,14 @@ __device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n
   y = warp_sum(y);
   if ((threadIdx.x & 31) == 0) {
     red[threadIdx.x >> 5] = x;
-    red[kWarps + (threadIdx.x >> 5)] = y;
+    red[kW + (threadIdx.x >> 5)] = y;
   }
   __syncthreads();
   longlong2 r = {0, 0};
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kW; ++w) {
     r.x += red[w];
-    r.y += red[kWarps + w];
+    r.y += red[kW + w];
   }
   return r;
 }
@@ -226,7 +227,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     b = start_b;
     base = start_base;
   } else {
-    const long long total = units_before<R>(p, p.a.batch, p.a.batch, red).y;
+    const long long total = units_before<R, kWarps>(p, p.a.batch, p.a.batch, red).y;
     const long long per = units_per_cta(total, p.ctas);
     cur = per * blockIdx.x;
     end = min(total, cur + per);
@@ -659,80 +660,97 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   }
 }
 
-// One CTA per row of an item: adds up the partial results of an item that was
-// cut, in the order of its CTAs.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ Params p, int blocks) {
+// A CTA for RC rows of an item (8, or 1 where there are few items): adds up the
+// partial results of an item that was cut, in an order that depends on their
+// number alone.  D / 4 lanes take 4 elements each of the rows of a piece, the
+// CTA's 8 warps every kStripes-th piece.
+constexpr int kJoinWarps = 8;
+
+template <int D, int NT, int RC>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ Params p) {
   constexpr int R = 8 * NT;
-  __shared__ long long red[2 * kWarps];
+  constexpr int kLanes = D / 4, kStripes = kJoinWarps * 32 / kLanes;
+  __shared__ long long red[2 * kJoinWarps];
+  __shared__ float2 ml_s[kJoinWarps][RC];
+  __shared__ float4 acc_s[kStripes][RC][kLanes];
   const int b = blockIdx.y;
   const Seq s = sequence<R>(p, b);
-  const int row = blockIdx.x % R, item = blockIdx.x / R;
+  const int r0 = blockIdx.x % (R / RC) * RC, item = blockIdx.x / (R / RC);
   const int h = item % p.a.c.kv_heads, rb = item / p.a.c.kv_heads;
+  const int rows = min(RC, s.lq * p.group - rb * R - r0);
   // Every CTA waits for kv_rows_kernel before it ends, also where it has
   // nothing to add up: what follows on the stream waits for this kernel only.
   auto rows_done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
-  if (rb >= s.blocks || rb * R + row >= s.lq * p.group) return rows_done();
-  const longlong2 units = units_before<R>(p, b, p.a.batch, red);
-  const long long base = units.x, total = units.y;
-  const long long per = units_per_cta(total, p.ctas);
-  const long long first = base + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
-  const long long c0 = first / per, c1 = last / per;
+  if (rb >= s.blocks || rows <= 0) return rows_done();
+  const longlong2 units = units_before<R, kJoinWarps>(p, b, p.a.batch, red);
+  const long long per = units_per_cta(units.y, p.ctas);
+  const long long first = units.x + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
+  const int c0 = static_cast<int>(first / per), pieces = static_cast<int>(last / per) - c0 + 1;
   rows_done();
-  if (c0 == c1) return;
-  auto at = [&](long long cta) {
-    const int slot = cta * per <= first ? 1 : 0;
-    return (cta * 2 + slot) * R + row;
+  if (pieces == 1) return;
+  // first of the RC rows of a piece; the one that holds the item's start lies in slot 1
+  auto at = [&](int piece) { return ((static_cast<long long>(c0) + piece) * 2 + (piece == 0 ? 1 : 0)) * R + r0; };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // maximum m and sum l of row lane % RC: over pieces, lanes, warps
+  auto add = [](float& m, float& l, float m2, float l2) {
+    const float top = fmaxf(m, m2);
+    l = l * (m == top ? 1.0f : exp2_approx(m - top)) + l2 * (m2 == top ? 1.0f : exp2_approx(m2 - top));
+    m = top;
   };
-  // maximum and sum over the pieces
-  __shared__ float sm[kWarps], sl[kWarps];
-  float m = -INFINITY;
-  for (long long cta = c0 + threadIdx.x; cta <= c1; cta += kThreads) m = fmaxf(m, p.partial_ml[at(cta) * 2]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float l = 0.0f;
-  for (long long cta = c0 + threadIdx.x; cta <= c1; cta += kThreads) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + at(cta) * 2);
-    l += ml.y * (ml.x == m ? 1.0f : exp2_approx(ml.x - m));
+  float m = -INFINITY, l = 0.0f;
+  for (int i = threadIdx.x / RC; i < pieces; i += 32 * kJoinWarps / RC) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + (at(i) + threadIdx.x % RC) * 2);
+    add(m, l, ml.x, ml.y);
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  if ((threadIdx.x & 31) == 0) sl[threadIdx.x >> 5] = l;
-  __syncthreads();
-  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-  // lane i of warp w: 4 elements of every kWarps-th piece
-  __shared__ float4 acc_s[kWarps][D / 4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane < D / 4) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long cta = c0 + warp; cta <= c1; cta += kWarps) {
-      const float mw = p.partial_ml[at(cta) * 2];
-      const float z = mw == m ? 1.0f : exp2_approx(mw - m);
-      const float4 v = *reinterpret_cast<const float4*>(p.partial + at(cta) * D + 4 * lane);
-      acc.x += z * v.x, acc.y += z * v.y, acc.z += z * v.z, acc.w += z * v.w;
-    }
-    acc_s[warp][lane] = acc;
+  for (int o = RC; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    add(m, l, m2, l2);
   }
+  if (lane < RC) ml_s[warp][lane] = make_float2(m, l);
   __syncthreads();
-  if (threadIdx.x < D / 4) {
-    float4 acc = acc_s[0][threadIdx.x];
+  m = -INFINITY;
+  l = 0.0f;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      const float4 v = acc_s[w][threadIdx.x];
-      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-    }
-    write_row(p, s, h, rb * R + row, 4 * threadIdx.x, acc, l == 0.0f ? 0.0f : p.a.c.v_S[h] / l);
-    if (threadIdx.x == 0) write_lse(p, s, h, rb * R + row, m, l);
-  }
-}
+  for (int w = 0; w < kJoinWarps; ++w) add(m, l, ml_s[w][lane % RC].x, ml_s[w][lane % RC].y);
 
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
+  const int el = threadIdx.x % kLanes, stripe = threadIdx.x / kLanes;
+  float4 acc[RC] = {};
+#pragma unroll 4
+  for (int i0 = 0; i0 < pieces; i0 += kStripes) {  // (whole warps stay together for the shuffles)
+    const int i = i0 + stripe;
+    const bool have = i < pieces;
+    const long long row0 = at(have ? i : 0);
+    // weight of row lane % RC of this lane's piece (D = 64: a warp has two)
+    const float mi = p.partial_ml[(row0 + lane % RC) * 2];
+    const float z = !have ? 0.0f : (mi == m ? 1.0f : exp2_approx(mi - m));
+#pragma unroll
+    for (int r = 0; r < RC; ++r) {
+      const float zr = __shfl_sync(0xFFFFFFFFu, z, (lane / kLanes * kLanes + r) & 31);
+      if (have) {
+        const float4 v = *reinterpret_cast<const float4*>(p.partial + (row0 + r) * D + 4 * el);
+        acc[r].x += zr * v.x, acc[r].y += zr * v.y, acc[r].z += zr * v.z, acc[r].w += zr * v.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RC; ++r) acc_s[stripe][r][el] = acc[r];
+  __syncthreads();
+  const float vS = p.a.c.v_S[h];
+  // (RC kLanes is a multiple of 32 or less than a warp's worth: warp 0 alone)
+  for (int i = threadIdx.x; i < (RC * kLanes + 31) / 32 * 32; i += 32 * kJoinWarps) {
+    const int r = i / kLanes, e = i % kLanes;
+    const float mr = __shfl_sync(0xFFFFFFFFu, m, r % RC), lr = __shfl_sync(0xFFFFFFFFu, l, r % RC);
+    if (r >= rows) continue;
+    float4 a = acc_s[0][r][e];
+#pragma unroll
+    for (int w = 1; w < kStripes; ++w) {
+      const float4 v = acc_s[w][r][e];
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+    write_row(p, s, h, rb * R + r0 + r, 4 * e, a, lr == 0.0f ? 0.0f : vS / lr);
+    if (e == 0) write_lse(p, s, h, rb * R + r0 + r, mr, lr);
+  }
 }
 
 // Rows per item: the fewest 8-row tiles that hold all rows of a sequence.
@@ -745,10 +763,12 @@ struct Plan {
   int nt, ctas;   // its 8-row tiles and CTAs
   int limit;
   bool prompt;
+  int num_sms;
 };
 
 Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int num_sms) {
   Plan p;
+  p.num_sms = num_sms;
   const int64_t rows = max_q * (q_heads / kv_heads);
   p.prompt = rows > kRowsLimit;
   p.limit = p.prompt ? kRowsLimit : 0x7FFFFFFF;
@@ -774,17 +794,23 @@ cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the joining kernel is launched while the first still runs (programmatic
   // dependent launch) and waits for its end on the device
-  const int blocks = static_cast<int>((plan.rows + R - 1) / R);
+  const int64_t items = (plan.rows + R - 1) / R * p.a.c.kv_heads;
+  // 8 rows a CTA read a piece's rows together; where that leaves SMs without a
+  // CTA, a row a CTA shortens the walk over the pieces (two sequences of
+  // 131072 tokens, 16 items of 47 pieces: 72 us with 8 rows a CTA, 66 with 1;
+  // 48 of 8192: 60 us with 8, 64 with 1)
+  const bool few = items * NT * p.a.batch < plan.num_sms;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks) * p.a.c.kv_heads * R, static_cast<unsigned>(p.a.batch));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(items * (few ? R : NT)), static_cast<unsigned>(p.a.batch));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, static_cast<const Params&>(p), blocks);
+  return few ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 1>, static_cast<const Params&>(p))
+             : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8>, static_cast<const Params&>(p));
 }
 
 }  // namespace
