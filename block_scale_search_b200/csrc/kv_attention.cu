@@ -764,10 +764,12 @@ struct Plan {
   int limit;
   bool prompt;
   int num_sms;
+  PromptPlan prompts;
+  size_t rows_bytes, prompt_bytes;  // of the workspace
 };
 
-Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int num_sms) {
-  Plan p;
+Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int head_dim, int num_sms) {
+  Plan p{};
   p.num_sms = num_sms;
   const int64_t rows = max_q * (q_heads / kv_heads);
   p.prompt = rows > kRowsLimit;
@@ -779,6 +781,11 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(p.nt);
   const double want = tiles / kWarps + 1.0;
   p.ctas = static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
+  p.rows_bytes = (static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
+  if (p.prompt) {
+    p.prompts = prompt_plan(batch, rows, max_kv, kv_heads, num_sms);
+    p.prompt_bytes = prompt_workspace_bytes(p.prompts, head_dim);
+  }
   return p;
 }
 
@@ -817,13 +824,13 @@ cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
 
 size_t kv_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                     int kv_heads, int head_dim, int num_sms) {
-  const Plan p = plan_of(batch, max_q, max_kv, q_heads, kv_heads, num_sms);
-  return static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float);
+  const Plan p = plan_of(batch, max_q, max_kv, q_heads, kv_heads, head_dim, num_sms);
+  return p.rows_bytes + p.prompt_bytes;
 }
 
 cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_sms, cudaStream_t stream) {
   if (a.batch == 0 || a.total_q == 0) return cudaSuccess;
-  const Plan plan = plan_of(a.batch, a.max_q, a.max_kv, a.q_heads, a.c.kv_heads, num_sms);
+  const Plan plan = plan_of(a.batch, a.max_q, a.max_kv, a.q_heads, a.c.kv_heads, a.c.head_dim, num_sms);
   Params p{};
   p.a = a;
   p.group = a.q_heads / a.c.kv_heads;
@@ -833,7 +840,7 @@ cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_s
   p.ctas = plan.ctas;
   p.rows_limit = plan.limit;
   if (plan.prompt) {
-    const cudaError_t e = launch_kv_prompt(p, stream);
+    const cudaError_t e = launch_kv_prompt(p, plan.prompts, static_cast<char*>(workspace) + plan.rows_bytes, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.c.head_dim == 128) {

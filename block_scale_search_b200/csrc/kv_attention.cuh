@@ -19,7 +19,9 @@ struct Params {
   float* partial_ml;
   int ctas;
   int rows_limit;  // kv_rows_kernel serves sequences with at most so many query rows for a KV head
-  int row_blocks;  // of kv_prompt_kernel
+  int row_blocks, splits;  // of kv_prompt_kernel
+  float* split_o;          // [item][split][256][D] sums, and their maxima and sums
+  float2* split_ml;
 };
 
 // Raises a kernel's limit of dynamic shared memory, once per device.
@@ -37,8 +39,15 @@ struct SmemOptIn {
   }
 };
 
-// Prompts (kv_prompt.cu).
-cudaError_t launch_kv_prompt(Params& p, cudaStream_t stream);
+// Prompts (kv_prompt.cu): how a call's items (256 query rows of a sequence and
+// KV head) are laid over CTAs, and the launch.
+struct PromptPlan {
+  int64_t row_blocks, items;
+  int splits;
+};
+PromptPlan prompt_plan(int64_t batch, int64_t rows, int64_t max_kv, int kv_heads, int num_sms);
+size_t prompt_workspace_bytes(const PromptPlan& plan, int head_dim);
+cudaError_t launch_kv_prompt(Params& p, const PromptPlan& plan, void* workspace, cudaStream_t stream);
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -228,10 +228,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
   const nvfp4_kv_cache& c = p.a.c;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  // the longest items (a sequence's last rows) first
+  // the longest items (a sequence's last rows) first, their splits side by side
   const int per_block = p.a.batch * c.kv_heads;
-  const int rb = p.row_blocks - 1 - static_cast<int>(blockIdx.x) / per_block;
-  const int bh = static_cast<int>(blockIdx.x) % per_block;
+  const int item = static_cast<int>(blockIdx.x) / p.splits, split = static_cast<int>(blockIdx.x) % p.splits;
+  const int rb = p.row_blocks - 1 - item / per_block;
+  const int bh = item % per_block;
   const int b = bh / c.kv_heads, h = bh % c.kv_heads;
   const Span s = span_of(p, b);
   const int rows = s.lq * p.group, r0 = rb * kRows;
@@ -241,8 +242,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
   int lo, hi, unused;
   visible(p, s, r0, lo, unused);
   visible(p, s, min(r0 + kRows, rows) - 1, unused, hi);
-  const int first = lo / kTokens;
-  const int steps = hi > lo ? (hi + kTokens - 1) / kTokens - first : 0;
+  const int all_first = lo / kTokens;
+  const int all_steps = hi > lo ? (hi + kTokens - 1) / kTokens - all_first : 0;
+  // and this CTA's part of them
+  const int begin = static_cast<int>(static_cast<int64_t>(all_steps) * split / p.splits);
+  const int first = all_first + begin;
+  const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (split + 1) / p.splits) - begin;
 
   auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
   if (threadIdx.x == 0) {
@@ -419,7 +424,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     }
     uint32_t nan_blocks = 0;  // bit i: a visible V of elements 16 i .. is NaN
     if (*reinterpret_cast<volatile int*>(&sh.nan_v) && have) {
-      for (int tk = vlo; tk < vhi; ++tk) {
+      const int tk1 = min(vhi, (first + steps) * kTokens);
+      for (int tk = max(vlo, first * kTokens); tk < tk1; ++tk) {
         const int id = row_table[tk >> p.page_shift];
         if (id < 0 || id >= c.num_pages) continue;
         const uint8_t* sc = c.v_scales + id * c.scale_page_stride +
@@ -429,6 +435,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     }
     if (m == -INFINITY) l = 0.0f;  // saw no token (the sum may hold some 2^-126)
     const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + t) * kTileRows + (threadIdx.x & 127);
+    if (p.splits > 1 && have) {
+      // (a NaN maximum goes into the sum: the joining maximum passes over it)
+      p.split_ml[at] = m != m ? make_float2(0.0f, m) : make_float2(m, l);
+    }
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       uint32_t x[32];
@@ -443,15 +454,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if ((nan_blocks >> (2 * q + j / 16)) & 1) x[j] = 0x7FC00000u;
+        if (p.splits > 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          write_row(p, s, h, row, 32 * q + 4 * j,
-                    make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
-                                __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])),
-                    inv);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(p.split_o + at * D + 32 * q + 4 * j) =
+                make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            write_row(p, s, h, row, 32 * q + 4 * j,
+                      make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                                  __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])),
+                      inv);
+        }
       }
     }
-    if (have) write_lse(p, s, h, row, m, l);
+    if (have && p.splits == 1) write_lse(p, s, h, row, m, l);
     tc_fence_before();
   } else if (warp < 12) {
     // ------------------------------------------------------------- decode
@@ -639,23 +657,102 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// Adds up the splits of an item: a warp a row, at most 32 splits.
+constexpr int kJoinRows = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4;  // of a row; D = 64: half warps take every other split
+  const int lane = threadIdx.x & 31;
+  const int item = blockIdx.x, in_item = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int per_block = p.a.batch * p.a.c.kv_heads;
+  const int rb = p.row_blocks - 1 - item / per_block, bh = item % per_block;
+  const int b = bh / p.a.c.kv_heads, h = bh % p.a.c.kv_heads;
+  const Span s = span_of(p, b);
+  const int rows = s.lq * p.group, row = rb * kRows + in_item;
+  if (rows <= p.rows_limit || row >= rows) return;
+  auto at = [&](int split) { return (static_cast<int64_t>(item) * p.splits + split) * kRows + in_item; };
+  const float2 ml = lane < p.splits ? p.split_ml[at(lane)] : make_float2(-INFINITY, 0.0f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  // splits that saw no token are left out
+  const float z = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
+  float l = z * ml.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  const int el = lane % kLanes, half = lane / kLanes;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i0 = 0; i0 < p.splits; i0 += 32 / kLanes) {
+    const int i = i0 + half;
+    const float zi = __shfl_sync(0xFFFFFFFFu, z, i & 31);
+    if (i < p.splits && zi != 0.0f) {
+      const float4 v = *reinterpret_cast<const float4*>(p.split_o + at(i) * D + 4 * el);
+      acc.x += zi * v.x, acc.y += zi * v.y, acc.z += zi * v.z, acc.w += zi * v.w;
+    }
+  }
+  if constexpr (kLanes == 16) {
+    acc.x += __shfl_xor_sync(0xFFFFFFFFu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xFFFFFFFFu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xFFFFFFFFu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xFFFFFFFFu, acc.w, 16);
+  }
+  if (half == 0) write_row(p, s, h, row, 4 * el, acc, l == 0.0f ? 0.0f : p.a.c.v_S[h] / l);
+  if (lane == 0) write_lse(p, s, h, row, m, l);
+}
+
 template <int D>
 cudaError_t run_prompt(const Params& p, cudaStream_t stream) {
   constexpr int smem = Layout<D>::kBytes + 1024;
   static SmemOptIn opt_in;
   const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(&kv_prompt_kernel<D>), smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  kv_prompt_kernel<D><<<static_cast<unsigned>(grid), kPromptThreads, smem, stream>>>(p);
+  const int64_t items = static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads;
+  if (items * p.splits > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  kv_prompt_kernel<D><<<static_cast<unsigned>(items * p.splits), kPromptThreads, smem, stream>>>(p);
+  const cudaError_t r = cudaGetLastError();
+  if (r != cudaSuccess || p.splits == 1) return r;
+  kv_prompt_join_kernel<D><<<dim3(static_cast<unsigned>(items), kRows / kJoinRows), 32 * kJoinRows, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_prompt(Params& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.a.max_q) * p.group;
-  p.row_blocks = static_cast<int>((rows + kRows - 1) / kRows);
+// Splits of an item's steps: where a call has fewer items than SMs, each is
+// given to several CTAs.  The number with the shortest estimate, in steps of
+// 256 rows by 128 tokens (1.7 us at head_dim 128): every wave of CTAs takes its
+// share of steps and about 4 more to start and finish; partial results cost
+// about 2 a wave's worth of them, and the joining kernel 3.  One sequence of 64
+// new tokens over 32000, 64 / 8 heads of 128, takes 428 us unsplit.
+PromptPlan prompt_plan(int64_t batch, int64_t rows, int64_t max_kv, int kv_heads, int num_sms) {
+  PromptPlan best{};
+  best.row_blocks = (rows + kRows - 1) / kRows;
+  best.items = best.row_blocks * batch * kv_heads;
+  best.splits = 1;
+  const int64_t steps = (max_kv + kTokens - 1) / kTokens;
+  double least = 0.0;
+  for (int n = 1; n <= 32 && (n == 1 || (best.items * n <= 4 * num_sms && steps >= 2 * n)); ++n) {
+    const double waves = static_cast<double>((best.items * n + num_sms - 1) / num_sms);
+    double cost = waves * (static_cast<double>((steps + n - 1) / n) + 4.0);
+    if (n > 1) cost += 3.0 + 2.0 * static_cast<double>(best.items * n) / num_sms;
+    if (n == 1 || cost < least) {
+      least = cost;
+      best.splits = n;
+    }
+  }
+  return best;
+}
+
+size_t prompt_workspace_bytes(const PromptPlan& plan, int head_dim) {
+  return plan.splits == 1 ? 0 : static_cast<size_t>(plan.items) * plan.splits * kRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv_prompt(Params& p, const PromptPlan& plan, void* workspace, cudaStream_t stream) {
+  p.row_blocks = static_cast<int>(plan.row_blocks);
+  p.splits = plan.splits;
+  p.split_o = static_cast<float*>(workspace);
+  p.split_ml = reinterpret_cast<float2*>(p.split_o + plan.items * plan.splits * kRows * p.a.c.head_dim);
   return p.a.c.head_dim == 128 ? run_prompt<128>(p, stream) : run_prompt<64>(p, stream);
 }
 
