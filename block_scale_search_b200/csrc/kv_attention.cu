@@ -50,8 +50,13 @@ constexpr int kStages = 2;   // tiles of a warp's ring
 // What starting and finishing an item costs a CTA, in tiles: its page ids and
 // queries arrive in two trips to memory, its warps meet twice at the end.
 constexpr int kItemCost = 10;
-// Query rows of a sequence and KV head up to which this kernel serves it.
-constexpr int64_t kRowsLimit = 32;
+// Query rows of a sequence and KV head up to which this kernel serves it, in
+// blocks of 32; kv_prompt_kernel takes those with more.  Measured on 64 / 8
+// heads, 1 to 64 sequences of 500 to 32000 tokens: 32 rows take 12 to 157 us
+// here and 19 to 261 us there at head_dim 128, 64 rows (two blocks, the cache
+// decoded twice) 13 to 294 and 19 to 264; at head_dim 64, where a step of the
+// other kernel costs nearly as much, 64 rows take 10 to 178 and 17 to 223.
+constexpr int64_t rows_limit(int head_dim) { return head_dim == 64 ? 64 : 32; }
 
 // Resident CTAs the kernel is built for (its registers and shared memory).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : (nt == 2 ? 4 : 2); }
@@ -772,9 +777,10 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   Plan p{};
   p.num_sms = num_sms;
   const int64_t rows = max_q * (q_heads / kv_heads);
-  p.prompt = rows > kRowsLimit;
-  p.limit = p.prompt ? kRowsLimit : 0x7FFFFFFF;
-  p.rows = p.prompt ? kRowsLimit : rows;
+  const int64_t limit = rows_limit(head_dim);
+  p.prompt = rows > limit;
+  p.limit = static_cast<int>(limit);
+  p.rows = p.prompt ? limit : rows;
   p.nt = row_tiles(p.rows);
   const double tiles = static_cast<double>(batch) * kv_heads * static_cast<double>((p.rows + 8 * p.nt - 1) / (8 * p.nt)) *
                        static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);

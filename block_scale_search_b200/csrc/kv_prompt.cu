@@ -81,8 +81,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
-// Waits for a phase, for a quarter of a second at most: a wait given up is
-// counted and ends all later ones of the CTA, which then runs to its end.
+// Waits for a phase, for about two seconds at most: a wait given up is counted
+// and ends all later ones of the CTA, which then runs to its end.
 template <int kSleep>
 __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
   long long t0 = 0;
@@ -92,16 +92,22 @@ __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_
     if ((n & 255u) != 0) continue;
     if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
     if (t0 == 0) t0 = clock64();
-    if (clock64() - t0 > (1ll << 29)) {
+    if (clock64() - t0 > (1ll << 32)) {
       atomicAdd(&g_stalls, 1u);
       *reinterpret_cast<volatile int*>(&sh->gave_up) = 1;
       return;
     }
   }
 }
-// kSleep: ns between tries; a warp that tries without a pause takes an issue
-// slot in four from the warps that work.
+// kSleep: ns between tries, which leaves issue slots to the warps that work.
 constexpr int kSoftmaxSleep = 20, kDecodeSleep = 100;
+// Waits for MMAs in flight before TMEM is given back, also after a wait was
+// given up (then for a tenth of a second at most).
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity) && clock64() - t0 < (1ll << 28)) {
+  }
+}
 template <int kSleep = 0>
 __device__ __forceinline__ void mbar_wait(Shared* sh, uint32_t bar, uint32_t parity) {
   if (!mbar_try(bar, parity)) mbar_wait_slow<kSleep>(sh, bar, parity);
@@ -249,6 +255,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
   const int first = all_first + begin;
   const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (split + 1) / p.splits) - begin;
 
+  const int tiles = rows - r0 > kTileRows ? 2 : 1;  // with rows in them
   auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -329,7 +336,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     };
     int page = page_of(0);
     float m = -INFINITY, down = 0.0f, l = 0.0f;
-    for (int i = 0; i < steps; ++i) {
+    const int my_steps = t < tiles ? steps : 0;
+    for (int i = 0; i < my_steps; ++i) {
       const int tb = (first + i) * kTokens;
       const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
       page = page_of(i + 1);
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       mbar_arrive(bar(kPFull + 2 * t + 1));
     }
     // -------------------------------------------------------------- result
-    if (steps > 0) {
+    if (my_steps > 0) {
       mbar_wait(&sh, bar(kOFull + t), 0);
       tc_fence_after();
       mbar_wait(&sh, bar(kScan), 0);
@@ -443,7 +451,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       uint32_t x[32];
-      if (steps > 0) {
+      if (my_steps > 0) {
         tmem_load32(o_col + 32 * q, x);
         tmem_wait_load();
       } else {
@@ -586,6 +594,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       there = next_there;
       slot = free_slot;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (nan_v) *reinterpret_cast<volatile int*>(&sh.nan_v) = 1;
     mbar_arrive(bar(kScan));
   } else {
@@ -605,50 +614,56 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         }
         tc_commit(bar(kSFull + t));
       };
+      auto pv = [&](int t, int st, int k0, int k1, bool add) {
+        const uint64_t v0 = v_desc + st * kTileStep;
+#pragma unroll
+        for (int k = k0; k < k1; ++k)
+          mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, add || k > 0);
+      };
       mbar_wait(&sh, bar(kKFull), 0);
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < tiles; ++t) {
         mbar_wait(&sh, bar(kQFull + t), 0);
         tc_fence_after();
-        if (elect_one()) qk(t, 0);
+        if (elect_one()) {
+          qk(t, 0);
+          if (t == tiles - 1) tc_commit(bar(kKEmpty));
+        }
         __syncwarp();
       }
-      if (elect_one()) tc_commit(bar(kKEmpty));
-      __syncwarp();
+      // One warp issues for both tiles, in turn: with a warp each their MMAs
+      // mix and both tiles wait for both (631 us instead of 502 for 4 x 2048
+      // rows over 8192).
       for (int i = 0; i < steps; ++i) {
         const int st = i & 1, nst = st ^ 1;
-        for (int t = 0; t < 2; ++t) {
-          if (t == 0) mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
-          if (t == 0 && i + 1 < steps) mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
-          const uint64_t v0 = v_desc + st * kTileStep;
+        const bool more = i + 1 < steps;
+        mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
+        if (more) mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
+        for (int t = 0; t < tiles; ++t) {
           mbar_wait(&sh, bar(kPFull + 2 * t), i & 1);
           tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kTokens / 32; ++k)
-              mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, i > 0 || k > 0);
-          }
+          if (elect_one()) pv(t, st, 0, kTokens / 32, i > 0);
           __syncwarp();
           mbar_wait(&sh, bar(kPFull + 2 * t + 1), i & 1);
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
-            for (int k = kTokens / 32; k < kTokens / 16; ++k)
-              mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, i > 0 || k > 0);
-            if (i + 1 < steps)
+            pv(t, st, kTokens / 32, kTokens / 16, true);
+            if (more)
               qk(t, nst);
             else
               tc_commit(bar(kOFull + t));
-            if (t == 1) {
+            if (t == tiles - 1) {
               tc_commit(bar(kVEmpty + st));
-              if (i + 1 < steps) tc_commit(bar(kKEmpty + nst));
+              if (more) tc_commit(bar(kKEmpty + nst));
             }
           }
           __syncwarp();
         }
       }
       // nothing of this CTA's is in flight when it ends
-      mbar_wait(&sh, bar(kOFull + 0), 0);
-      mbar_wait(&sh, bar(kOFull + 1), 0);
+      for (int t = 0; t < tiles; ++t) {
+        mbar_wait(&sh, bar(kOFull + t), 0);
+        mbar_drain(bar(kOFull + t), 0);
+      }
     }
   }
   __syncthreads();
