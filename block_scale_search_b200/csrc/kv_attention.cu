@@ -113,36 +113,51 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
   return s;
 }
 
+// (The host refuses calls whose bounds allow 2^31 units: a 64-bit division here
+// is a call, for which the whole kernel would save registers to memory.)
 template <int R>
-__device__ __forceinline__ long long seq_units(const Params& p, int b) {
+__device__ __forceinline__ int seq_units(const Params& p, int b) {
   const Seq s = sequence<R>(p, b);
-  return static_cast<long long>(s.blocks) * p.a.c.kv_heads * s.span;
+  return s.blocks * p.a.c.kv_heads * s.span;
 }
 
-__device__ __forceinline__ long long warp_sum(long long v) {
+__device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += up;
   }
   return v;
 }
 
-// Sums of seq_units over b < n1 (x) and b < n2 (y), n1 <= n2, by the whole CTA
-// of kW warps (every thread
-// gets them).  red: 2 kW.
+// Sum of seq_units over all sequences, by the whole CTA (every thread gets it).
+template <int R>
+__device__ __forceinline__ int all_units(const Params& p, int* red) {
+  int v = 0;
+  for (int b = threadIdx.x; b < p.a.batch; b += kThreads) v += seq_units<R>(p, b);
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += red[w];
+  return v;
+}
+
+// Sums of seq_units over the sequences before n (x) and over all (y), by a CTA
+// of kW warps (every thread gets them).  red: 2 kW.
 template <int R, int kW>
-__device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n2, long long* red) {
-  long long x = 0, y = 0;
-  for (int b = threadIdx.x; b < n2; b += 32 * kW) {
-    const long long n = seq_units<R>(p, b);
-    y += n;
-    if (b < n1) x += n;
+__device__ __forceinline__ int2 units_before(const Params& p, int n, int* red) {
+  int x = 0, y = 0;
+  for (int b = threadIdx.x; b < p.a.batch; b += 32 * kW) {
+    const int u = seq_units<R>(p, b);
+    y += u;
+    if (b < n) x += u;
   }
   x = warp_sum(x);
   y = warp_sum(y);
@@ -151,7 +166,7 @@ __device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n
     red[kW + (threadIdx.x >> 5)] = y;
   }
   __syncthreads();
-  longlong2 r = {0, 0};
+  int2 r = {0, 0};
 #pragma unroll
   for (int w = 0; w < kW; ++w) {
     r.x += red[w];
@@ -160,16 +175,8 @@ __device__ __forceinline__ longlong2 units_before(const Params& p, int n1, int n
   return r;
 }
 
-// a / b for b > 0, a >= 0; the 64-bit division is long and hardly ever needed
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return (a >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
-
 // Units per CTA: an equal share, but no less than a tile a warp.
-__device__ __forceinline__ long long units_per_cta(long long total, int ctas) {
-  const long long share = quotient(total + ctas - 1, ctas);
-  return share > kWarps ? share : kWarps;
-}
+__device__ __forceinline__ int units_per_cta(int total, int ctas) { return max((total + ctas - 1) / ctas, kWarps); }
 
 // Of a query row of the item: factor of its scores (base 2), visible tokens.
 struct RowInfo {
@@ -189,7 +196,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join_o = reinterpret_cast<float*>(smem);
   float* const join_ml = join_o + kWarps * R * D;
-  __shared__ long long red[2 * kWarps];
+  __shared__ int red[kWarps];
   __shared__ RowInfo row_info[R];
 
   // from lane 0, so that the compiler takes it, and branches on it, as uniform
@@ -206,23 +213,26 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 
   // this CTA's piece of the line of work, and the sequence that holds its start
   __shared__ int start_b;
-  __shared__ long long start_base;
+  __shared__ int start_base;
   int b = 0;
-  long long base = 0, cur, end;  // base: first unit of sequence b
+  int base = 0, cur, end;  // base: first unit of sequence b
+  __shared__ int share;  // units per CTA, for the list of cut items
+  if (p.cut != nullptr && threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (p.a.batch <= kThreads) {   // a sequence a thread: one look at the lengths
-    const long long n = threadIdx.x < p.a.batch ? seq_units<R>(p, threadIdx.x) : 0;
-    long long inc = warp_scan(n, lane);
+    const int n = threadIdx.x < p.a.batch ? seq_units<R>(p, threadIdx.x) : 0;
+    int inc = warp_scan(n, lane);
     if (lane == 31) red[warp] = inc;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) inc += red[w];
       total += red[w];
     }
-    const long long per = units_per_cta(total, p.ctas);
+    const int per = units_per_cta(total, p.ctas);
     cur = per * blockIdx.x;
     end = min(total, cur + per);
+    if (threadIdx.x == 0) share = per;
     if (inc - n <= cur && cur < inc) {
       start_b = threadIdx.x;
       start_base = inc - n;
@@ -232,16 +242,17 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     b = start_b;
     base = start_base;
   } else {
-    const long long total = units_before<R, kWarps>(p, p.a.batch, p.a.batch, red).y;
-    const long long per = units_per_cta(total, p.ctas);
+    const int total = all_units<R>(p, red);
+    const int per = units_per_cta(total, p.ctas);
     cur = per * blockIdx.x;
     end = min(total, cur + per);
+    if (threadIdx.x == 0) share = per;  // (only that thread reads it)
     if (cur >= end) return;
     for (;; b += 32) {  // every warp scans 32 sequences at a time
       if (b >= p.a.batch) return;
       const int bb = b + lane;
-      const long long n = bb < p.a.batch ? seq_units<R>(p, bb) : 0;
-      const long long inc = warp_scan(n, lane);
+      const int n = bb < p.a.batch ? seq_units<R>(p, bb) : 0;
+      const int inc = warp_scan(n, lane);
       const unsigned past = __ballot_sync(0xFFFFFFFFu, base + inc > cur);
       if (past) {
         const int f = __ffs(past) - 1;
@@ -255,16 +266,14 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 
   while (cur < end) {
     const Seq s = sequence<R>(p, b);
-    const long long in_seq = cur - base;
-    const int item = static_cast<int>(quotient(in_seq, s.span));
-    const int us = static_cast<int>(in_seq - static_cast<long long>(item) * s.span);
-    const int ue = static_cast<int>(min(static_cast<long long>(s.span), us + (end - cur)));
+    const int in_seq = cur - base;
+    const int item = in_seq / s.span, us = in_seq - item * s.span, ue = min(s.span, us + (end - cur));
     const int ts = max(0, us - kItemCost), te = max(0, ue - kItemCost);  // this CTA's tiles of the item
     const int h = item % c.kv_heads, r0 = item / c.kv_heads * R;
     auto next_item = [&]() {  // false at the end of the batch
       cur += ue - us;
       if (cur >= end) return true;
-      long long n = seq_units<R>(p, b);
+      int n = seq_units<R>(p, b);
       while (cur >= base + n) {  // also steps over sequences without new tokens
         base += n;
         if (++b >= p.a.batch) return false;
@@ -633,6 +642,11 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     __syncthreads();
     const bool whole = ts == 0 && te == s.tiles;
     const int slot = ts == 0 ? 1 : 0;  // of a cut item: 0 where an earlier CTA has its start
+    if (p.cut != nullptr && ts == 0 && !whole && threadIdx.x == 0) {
+      // at most one item is cut behind its first tile in this CTA
+      // its last tile is tiles - te - 1 units behind this CTA's end
+      p.cut[blockIdx.x] = make_int4(b, item, blockIdx.x, (s.tiles - te - 1) / share + 2);
+    }
     const float vS = c.v_S[h];
     const int rows = min(R, s.lq * p.group - r0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
@@ -667,32 +681,47 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 
 // A CTA for RC rows of an item (8, or 1 where there are few items): adds up the
 // partial results of an item that was cut, in an order that depends on their
-// number alone.  D / 4 lanes take 4 elements each of the rows of a piece, the
+// number alone.  The items are all of the call's, whose pieces each CTA works
+// out while kv_rows_kernel still runs, or (kList) those that it listed as cut.  D / 4 lanes take 4 elements each of the rows of a piece, the
 // CTA's 8 warps every kStripes-th piece.
 constexpr int kJoinWarps = 8;
 
-template <int D, int NT, int RC>
+template <int D, int NT, int RC, bool kList>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ Params p) {
   constexpr int R = 8 * NT;
   constexpr int kLanes = D / 4, kStripes = kJoinWarps * 32 / kLanes;
-  __shared__ long long red[2 * kJoinWarps];
   __shared__ float2 ml_s[kJoinWarps][RC];
   __shared__ float4 acc_s[kStripes][RC][kLanes];
-  const int b = blockIdx.y;
-  const Seq s = sequence<R>(p, b);
-  const int r0 = blockIdx.x % (R / RC) * RC, item = blockIdx.x / (R / RC);
-  const int h = item % p.a.c.kv_heads, rb = item / p.a.c.kv_heads;
-  const int rows = min(RC, s.lq * p.group - rb * R - r0);
+  const int r0 = blockIdx.x % (R / RC) * RC;
   // Every CTA waits for kv_rows_kernel before it ends, also where it has
   // nothing to add up: what follows on the stream waits for this kernel only.
   auto rows_done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
-  if (rb >= s.blocks || rows <= 0) return rows_done();
-  const longlong2 units = units_before<R, kJoinWarps>(p, b, p.a.batch, red);
-  const long long per = units_per_cta(units.y, p.ctas);
-  const long long first = units.x + static_cast<long long>(item) * s.span + kItemCost, last = first + s.tiles - 1;
-  const int c0 = static_cast<int>(first / per), pieces = static_cast<int>(last / per) - c0 + 1;
-  rows_done();
-  if (pieces == 1) return;
+  Span s;
+  int b, item, c0, pieces;
+  if constexpr (kList) {
+    rows_done();
+    const int4 cut = p.cut[blockIdx.x / (R / RC)];
+    if (cut.w == 0) return;
+    b = cut.x, item = cut.y, c0 = cut.z, pieces = cut.w;
+    s = span_of(p, b);
+  } else {
+    __shared__ int red[2 * kJoinWarps];
+    b = blockIdx.y;
+    item = blockIdx.x / (R / RC);
+    const Seq seq = sequence<R>(p, b);
+    s = seq;
+    if (item >= seq.blocks * p.a.c.kv_heads) return rows_done();
+    const int2 units = units_before<R, kJoinWarps>(p, b, red);
+    const int per = units_per_cta(units.y, p.ctas);
+    const int first = units.x + item * seq.span + kItemCost;
+    c0 = first / per;
+    pieces = (first + seq.tiles - 1) / per - c0 + 1;
+    rows_done();
+    if (pieces == 1) return;
+  }
+  const int h = item % p.a.c.kv_heads, rb = item / p.a.c.kv_heads;
+  const int rows = min(RC, s.lq * p.group - rb * R - r0);
+  if (rows <= 0) return;
   // first of the RC rows of a piece; the one that holds the item's start lies in slot 1
   auto at = [&](int piece) { return ((static_cast<long long>(c0) + piece) * 2 + (piece == 0 ? 1 : 0)) * R + r0; };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -766,11 +795,14 @@ int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 struct Plan {
   int64_t rows;   // most rows that kv_rows_kernel gets of a sequence
   int nt, ctas;   // its 8-row tiles and CTAs
+  int items;      // its items of a sequence, at most
+  enum { kByRow, kByTile, kListed } join;
   int limit;
   bool prompt;
   int num_sms;
   PromptPlan prompts;
   size_t rows_bytes, prompt_bytes;  // of the workspace
+  bool fits;      // the work can be counted in 32 bits
 };
 
 Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_heads, int head_dim, int num_sms) {
@@ -782,15 +814,27 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   p.limit = static_cast<int>(limit);
   p.rows = p.prompt ? limit : rows;
   p.nt = row_tiles(p.rows);
-  const double tiles = static_cast<double>(batch) * kv_heads * static_cast<double>((p.rows + 8 * p.nt - 1) / (8 * p.nt)) *
-                       static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
+  p.items = static_cast<int>((p.rows + 8 * p.nt - 1) / (8 * p.nt)) * kv_heads;
+  // Joining: 8 rows a CTA read a piece's rows together; where that leaves SMs
+  // without a CTA, a row a CTA shortens the walk over the pieces (two sequences
+  // of 131072 tokens, 16 items of 47 pieces: 72 us with 8 rows a CTA, 67 with
+  // 1; 48 of 8192: 60 us with 8, 64 with 1).  Where items are many, looking at
+  // all lengths in every CTA costs more than a list of the cut ones (256
+  // sequences of up to 1000 tokens 65 us, with the list 59; 16 of 4100 with 16
+  // rows 17.5 and 18.9).
+  const int64_t join_ctas = static_cast<int64_t>(p.items) * batch * p.nt;
+  p.join = join_ctas < num_sms ? Plan::kByRow : (join_ctas <= 512 ? Plan::kByTile : Plan::kListed);
+  const double tiles = static_cast<double>(batch) * p.items * static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
+  p.fits = tiles < 0x7FF00000;
   const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(p.nt);
   const double want = tiles / kWarps + 1.0;
   p.ctas = static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
-  p.rows_bytes = (static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
+  p.rows_bytes = (static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float) +
+                  static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
   if (p.prompt) {
     p.prompts = prompt_plan(batch, rows, max_kv, kv_heads, num_sms);
     p.prompt_bytes = prompt_workspace_bytes(p.prompts, head_dim);
+    p.fits = p.fits && p.prompts.items * p.prompts.splits <= 0x7FFFFFFF;  // the grid
   }
   return p;
 }
@@ -803,18 +847,16 @@ cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
   cudaError_t e = opt_in.set(reinterpret_cast<const void*>(&kv_rows_kernel<D, NT>), smem);
   if (e != cudaSuccess) return e;
   p.partial_ml = p.partial + static_cast<int64_t>(p.ctas) * 2 * R * D;
+  p.cut = plan.join == Plan::kListed ? reinterpret_cast<int4*>(p.partial_ml + static_cast<int64_t>(p.ctas) * 2 * R * 2) : nullptr;
   kv_rows_kernel<D, NT><<<p.ctas, kThreads, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the joining kernel is launched while the first still runs (programmatic
   // dependent launch) and waits for its end on the device
-  const int64_t items = (plan.rows + R - 1) / R * p.a.c.kv_heads;
-  // 8 rows a CTA read a piece's rows together; where that leaves SMs without a
-  // CTA, a row a CTA shortens the walk over the pieces (two sequences of
-  // 131072 tokens, 16 items of 47 pieces: 72 us with 8 rows a CTA, 66 with 1;
-  // 48 of 8192: 60 us with 8, 64 with 1)
-  const bool few = items * NT * p.a.batch < plan.num_sms;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * (few ? R : NT)), static_cast<unsigned>(p.a.batch));
+  if (plan.join == Plan::kListed)
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas) * NT);
+  else
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.items * (plan.join == Plan::kByRow ? R : NT)), static_cast<unsigned>(p.a.batch));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -822,8 +864,10 @@ cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 1>, static_cast<const Params&>(p))
-             : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8>, static_cast<const Params&>(p));
+  const Params& args = p;
+  if (plan.join == Plan::kByRow) return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 1, false>, args);
+  if (plan.join == Plan::kByTile) return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8, false>, args);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, 8, true>, args);
 }
 
 }  // namespace
@@ -831,7 +875,7 @@ cudaError_t run_rows(Params& p, const Plan& plan, cudaStream_t stream) {
 size_t kv_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                     int kv_heads, int head_dim, int num_sms) {
   const Plan p = plan_of(batch, max_q, max_kv, q_heads, kv_heads, head_dim, num_sms);
-  return p.rows_bytes + p.prompt_bytes;
+  return p.fits ? p.rows_bytes + p.prompt_bytes : 0;
 }
 
 cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_sms, cudaStream_t stream) {

@@ -18,6 +18,7 @@ struct Params {
   float* partial;  // [CTA][2][R * D] sums, then [CTA][2][R * 2] maximum and sum
   float* partial_ml;
   int ctas;
+  int4* cut;       // [CTA]: sequence, item, first CTA and number of pieces (0: none) of a cut item; or NULL
   int rows_limit;  // kv_rows_kernel serves sequences with at most so many query rows for a KV head
   int row_blocks, splits;  // of kv_prompt_kernel
   float* split_o;          // [item][split][256][D] sums, and their maxima and sums

@@ -53,6 +53,7 @@ struct KvAttention {
   float scale;
 };
 
+// 0 for a call whose bounds allow more work than the kernels can count.
 size_t kv_attention_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                     int kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attention(const KvAttention& a, void* workspace, int num_sms,

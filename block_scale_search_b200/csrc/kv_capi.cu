@@ -180,9 +180,10 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* Q, int type, int
   if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
   const int sms = nvfp4::sm_count();
   if (sms <= 0) return nvfp4::record_cuda_status(cudaErrorNoDevice);
-  if (workspace_bytes < nvfp4::kv_attention_workspace_bytes(batch, max_q, max_kv, q_heads, cache->kv_heads,
-                                                            cache->head_dim, sms))
-    return NVFP4_ERR_WORKSPACE;
+  const size_t need =
+      nvfp4::kv_attention_workspace_bytes(batch, max_q, max_kv, q_heads, cache->kv_heads, cache->head_dim, sms);
+  if (need == 0) return NVFP4_ERR_SHAPE;
+  if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   nvfp4::KvAttention a{};
   a.c = *cache;
   a.Q = Q;

@@ -724,7 +724,6 @@ cudaError_t run_prompt(const Params& p, cudaStream_t stream) {
   const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(&kv_prompt_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads;
-  if (items * p.splits > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   kv_prompt_kernel<D><<<static_cast<unsigned>(items * p.splits), kPromptThreads, smem, stream>>>(p);
   const cudaError_t r = cudaGetLastError();
   if (r != cudaSuccess || p.splits == 1) return r;

@@ -693,7 +693,10 @@ int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t cod
  *              any lengths within them.
  *   causal     0 or 1; window >= 0, 0 for none; a window needs causal.
  *   batch      0 .. 65535; total_q, max_q < 2^31; q_heads a multiple of
- *              kv_heads, at most 1024.
+ *              kv_heads, at most 1024.  Bounds whose work the kernels cannot
+ *              count in 32 bits return NVFP4_ERR_SHAPE (batch * kv_heads *
+ *              (max_kv + 352) is to stay below 2^35, batch * q_heads * max_q
+ *              below 2^38).
  *   workspace  nvfp4_kv_attention_workspace_size() bytes (device dependent; 0
  *              for invalid arguments or no device), 256-byte aligned; needs no
  *              initialisation.  Calls that may overlap need one each.
