@@ -660,3 +660,159 @@ def test_serving_run(nv):
     nv.kv_copy_pages(pool, [25], [0])
     table[2, 5] = 0
     assert torch.equal(answer(Q2, [1, 1], lens3, [0, 2]), first)
+
+
+# ------------------------------------------------------ larger shapes, at random
+
+def reference_gpu(cache, Q, q_len, kv_len, table, causal, window):
+    """reference() for larger shapes: 64 bits on the GPU, a sequence and KV head at a time."""
+    total, heads, dim = Q.shape
+    kvh, page, scale = cache.kv_heads, cache.page_size, dim ** -0.5
+    G = heads // kvh
+    out = torch.zeros(total, heads, dim, dtype=torch.float64, device=DEV)
+    lse = torch.full((total, heads), float("-inf"), dtype=torch.float64, device=DEV)
+    tol_o, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
+    grid, e4m3 = GRID.to(DEV), e4m3_table().to(DEV)
+
+    def rows(codes, scales, S):
+        n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()
+        return grid[n] * e4m3[scales.long()].repeat_interleave(16, -1) * S.double()
+
+    row = 0
+    for b, (lq, lk) in enumerate(zip(q_len, kv_len)):
+        if lq and lk:
+            t = torch.arange(lk, device=DEV)
+            ids = table[b].to(DEV)[t // page].long()
+            p = (lk - lq + torch.arange(lq, device=DEV))[:, None]
+            see = (t <= p) if causal else torch.ones(lq, lk, dtype=torch.bool, device=DEV)
+            if window:
+                see = see & (t > p - window)
+            some = see.any(-1)
+            for h in range(kvh):
+                k = rows(cache.k_codes[ids, h, t % page], cache.k_scales[ids, h, t % page], cache.k_S[h])
+                v = rows(cache.v_codes[ids, h, t % page], cache.v_scales[ids, h, t % page], cache.v_S[h])
+                for g in range(G):
+                    q = Q[row:row + lq, h * G + g].double()
+                    x = (q @ k.T * scale).masked_fill(~see, float("-inf"))
+                    X = (q.abs() @ k.abs().T * scale).masked_fill(~see, 0).amax(-1)
+                    m = x.amax(-1).masked_fill(~some, 0)
+                    w = torch.exp(x - m[:, None])
+                    L = w.sum(-1).clamp(min=1e-300)
+                    o = w @ v / L[:, None]
+                    A = w @ v.abs() / L[:, None]
+                    d = 2 ** -18 * X + 2 ** -17
+                    at = (slice(row, row + lq), h * G + g)
+                    out[at] = o
+                    lse[at] = torch.where(some, m + torch.log(L), lse[at])
+                    tol_o[at] = (A * (2 ** -11 + 2 * d)[:, None] + see.sum(-1)[:, None] * 2 ** -25 * v.abs().max()
+                                 + o.abs() * torch.finfo(Q.dtype).eps / 2 + 1e-7)
+                    tol_l[at] = d + (m.abs() + torch.log(L).abs()) * 2 ** -21
+        row += lq
+    return out.cpu(), lse.cpu(), tol_o.cpu(), tol_l.cpu()
+
+
+def larger(nv, gen, q_len, kv_len, heads, kvh, dim, page, kind, causal=True, window=0, bounds=None):
+    pages, table = build_batch(gen, kv_len, page)
+    cache = make_cache(nv, gen, pages, page, kvh, dim)
+    Q = torch.randn(sum(q_len), heads, dim, generator=gen).to(kind).to(DEV)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(q_len)]), dtype=torch.int32, device=DEV)
+    lens = torch.tensor(kv_len, dtype=torch.int32, device=DEV)
+    mq, mk = bounds or (max(q_len), max(kv_len))
+    out, lse = nv.kv_attention(cache, Q, off, lens, table.to(DEV), mq, mk, None, causal, window, want_lse=True)
+    o, l, to, tl = reference_gpu(cache, Q, q_len, kv_len, table, causal, window)
+    check(lse, l, tl, "lse")
+    check(out, o, to, "out")
+
+
+@pytest.mark.parametrize("dim,heads,kvh,page", [(128, 8, 1, 16), (64, 8, 1, 64), (128, 4, 4, 32)])
+@pytest.mark.parametrize("q_len,kv_len", [([65], [9000]), ([300, 0, 40], [5000, 700, 3001]), ([129], [129]),
+                                          ([33, 33], [6001, 0])])
+def test_few_items_are_split(nv, dim, heads, kvh, page, q_len, kv_len):
+    gen = torch.Generator().manual_seed(dim + kv_len[0])
+    larger(nv, gen, q_len, kv_len, heads, kvh, dim, page, FP16)
+    larger(nv, gen, q_len, kv_len, heads, kvh, dim, page, BF16, window=700)
+    larger(nv, gen, q_len, kv_len, heads, kvh, dim, page, BF16, causal=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompts_and_single_tokens_together(nv, dim):
+    gen = torch.Generator().manual_seed(30 + dim)
+    larger(nv, gen, [1, 700, 1, 33, 1, 9, 0, 257], [4000, 900, 1, 2000, 17, 2500, 30, 257], 8, 2, dim, 16, BF16)
+
+
+@pytest.mark.parametrize("batch,kvh,heads", [(520, 2, 4), (200, 8, 8), (129, 1, 16), (90, 2, 64)])
+def test_many_sequences(nv, batch, kvh, heads):
+    """The cut items are joined from a list; batches over 128 are scheduled in steps."""
+    gen = torch.Generator().manual_seed(batch)
+    kv_len = (torch.randint(0, 700, (batch,), generator=gen) * (torch.rand(batch, generator=gen) < 0.9)).tolist()
+    larger(nv, gen, [1] * batch, kv_len, heads, kvh, 64 if batch % 2 else 128, 16, BF16)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_shapes(nv, seed):
+    gen = torch.Generator().manual_seed(1000 + seed)
+
+    def pick(*options):
+        return options[int(torch.randint(0, len(options), (1,), generator=gen))]
+
+    kvh, group, dim = pick(1, 2, 3, 5), pick(1, 2, 3, 4, 7, 8, 12, 16), pick(64, 128)
+    batch = pick(1, 2, 5, 40)
+    most = pick(1, 1, 2, 4, 9, 70, 200) if batch < 40 else pick(1, 2, 5)
+    q_len = torch.randint(0, most + 1, (batch,), generator=gen).tolist() if most > 1 else [1] * batch
+    q_len[0] = most
+    far = pick(30, 300, 3000) if batch < 40 else 400
+    kv_len = [int(torch.randint(max(0, n - 3), n + far, (1,), generator=gen)) for n in q_len]
+    causal = pick(True, True, True, False)
+    larger(nv, gen, q_len, kv_len, kvh * group, kvh, dim, pick(16, 32, 128), pick(BF16, FP16), causal=causal,
+           window=pick(0, 0, 1, 17, 250) if causal else 0,
+           bounds=(most + pick(0, 3), max(kv_len) + pick(0, 1)) if max(kv_len) else (most, 1))
+
+
+def test_nan_in_split_prompts(nv):
+    """A NaN V in one split's tokens reaches the rows that see it, through the join."""
+    gen = torch.Generator().manual_seed(40)
+    kv_len, lq, heads, kvh, dim = [5000], 40, 8, 1, 128
+    pages, table = build_batch(gen, kv_len, 16)
+    cache = make_cache(nv, gen, pages, 16, kvh, dim)
+    Q = torch.randn(lq, heads, dim, generator=gen).to(BF16).to(DEV)
+    off = torch.tensor([0, lq], dtype=torch.int32, device=DEV)
+    lens = torch.tensor(kv_len, dtype=torch.int32, device=DEV)
+    good = nv.kv_attention(cache, Q, off, lens, table.to(DEV), lq, 5000)
+    t = 5000 - 10                                   # position of query 30
+    cache.v_scales[table[0, t // 16], 0, t % 16, 3] = 0x7F
+    bad, lse = nv.kv_attention(cache, Q, off, lens, table.to(DEV), lq, 5000, want_lse=True)
+    assert torch.equal(bad[:30], good[:30])
+    nan = torch.isnan(bad[30:])
+    assert bool(nan[..., 48:64].all()) and not bool(nan[..., :48].any()) and not bool(nan[..., 64:].any())
+    assert not bool(torch.isnan(lse).any())
+    t = 100
+    cache.k_scales[table[0, t // 16], 0, t % 16, 0] = 0x7F
+    bad, lse = nv.kv_attention(cache, Q, off, lens, table.to(DEV), lq, 5000, want_lse=True)
+    assert bool(torch.isnan(bad).all()) and bool(torch.isnan(lse).all())
+
+
+def test_captured_page_copies(nv):
+    gen = torch.Generator().manual_seed(41)
+    cache = make_cache(nv, gen, 12, 16, 2, 64, layers=3)
+    src, dst = torch.tensor([1, 2], dtype=torch.int32), torch.tensor([7, 8], dtype=torch.int32)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        nv.kv_copy_pages(cache, src, dst)
+    src.fill_(3)                                    # the captured call keeps its own pages
+    cache.k_codes.copy_(torch.randint(0, 256, cache.k_codes.shape, generator=gen, dtype=torch.uint8))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_codes[:, 7], cache.k_codes[:, 1]) and torch.equal(cache.k_codes[:, 8], cache.k_codes[:, 2])
+
+
+def test_work_beyond_32_bits_is_refused(nv):
+    assert nv.nvfp4_kv_attention_workspace_size(60000, 1, 1 << 20, 64, 64, 128) == 0
+    assert nv.nvfp4_kv_attention_workspace_size(60000, 1 << 20, 1 << 10, 64, 64, 128) == 0
+    assert nv.nvfp4_kv_attention_workspace_size(1000, 1, 1 << 17, 64, 8, 128) > 0
+    cache = make_cache(nv, torch.Generator().manual_seed(0), 4, 16, 64, 128)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.nvfp4_kv_attention(cache.desc, z, 0, 64, 8, 8192, 128, z, z, z, 1 << 16, 60000, 1, 1 << 20, 0.1, 1, 0, z,
+                              8192, 128, None, torch.empty(1 << 12, dtype=torch.uint8, device=DEV), 1 << 40)
+    assert e.value.status == -2
