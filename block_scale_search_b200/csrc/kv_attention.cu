@@ -7,7 +7,7 @@
 //   out = sum_j e^(x_j - m) V_j / sum_j e^(x_j - m),   lse = log sum_j e^x_j
 // (no visible j: out = 0, lse = -inf).
 //
-// kv_rows_kernel: up to 8 NT query rows against one KV head, what decoding and
+// kv_rows_kernel: few query rows against one KV head, what decoding and
 // drafting ask for.  Bound by HBM (1.125 bytes per cached element, K and V)
 // with the 4-bit decode next, so the tensor work is arranged for few
 // instructions per cached element:
@@ -26,14 +26,22 @@
 //     the rounding of a 16-bit result); sums and the running maximum are FP32.
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
+// A tile of 32 tokens takes 670 instructions at head_dim 128 with 8 rows, 128
+// of them conversions, 128 products with scales and 32 MMAs (2, 2 and 8.5
+// cycles of a scheduler each), against 745 cycles of a scheduler's share of
+// HBM; in the loop it takes about 780, that is 6.3 TB/s.  Over a whole call
+// 4.1 TB/s (48 sequences of up to 8192 tokens, 64 / 8 heads of 128: 60 us) and
+// 4.5 TB/s (two of 131072: 67 us) remain: a CTA takes about 6 us until its
+// first tile is there (lengths, page ids and tiles are three trips to memory
+// one after another) and 2 us to join its warps, the cut items 3 to 5 us.
 //
 // Work split: the tiles (32 tokens) of all (sequence, row block, KV head)
 // items form one line; each CTA takes an equal piece of it, cutting items
 // where it must, so ragged batches and single long sequences fill the GPU
-// alike.  A CTA's warps take tiles in turn, each with its own ring of bulk
-// copies (16 rows of a page are contiguous).  An item inside one CTA is
-// finished there; of a cut item each CTA leaves a partial result (at most its
-// first and its last item), which kv_join_kernel adds up.
+// alike.  A CTA's warps take tiles in turn, each with its own ring of
+// asynchronous copies (16 rows of a page are contiguous).  An item inside one
+// CTA is finished there; of a cut item each CTA leaves a partial result (at
+// most its first and its last item), which kv_join_kernel adds up.
 #include <type_traits>
 
 #include "kv_attention.cuh"
@@ -58,8 +66,13 @@ constexpr int kItemCost = 10;
 // other kernel costs nearly as much, 64 rows take 10 to 178 and 17 to 223.
 constexpr int64_t rows_limit(int head_dim) { return head_dim == 64 ? 64 : 32; }
 
-// Resident CTAs the kernel is built for (its registers and shared memory).
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 5 : (nt == 2 ? 4 : 2); }
+// Resident CTAs the kernel is built for (its registers and shared memory).  More
+// warps are worth a few spilled registers: 16 rows at head_dim 128 take 102 us
+// with 4 CTAs and 180 bytes of spills, 105 with 3 and none (64 sequences of up
+// to 8000 tokens); with 5 and 550 bytes 153.
+__host__ __device__ constexpr int ctas_per_sm(int D, int nt) {
+  return nt == 1 ? 5 : (nt == 2 ? 4 : (D == 64 ? 3 : 2));
+}
 
 // Shared memory: the rings [warp][stage] and the queries' operands [8-row
 // tile][word][lane] of 16 bytes; once an item's tiles are used up, the join
@@ -185,7 +198,7 @@ struct RowInfo {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 kv_rows_kernel(const __grid_constant__ Params p) {
   constexpr int R = 8 * NT;
   constexpr int KW = D / 32;            // K words (8 values) per lane and row
@@ -287,7 +300,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     }
     const int mine = te - ts > warp ? (te - ts - warp + kWarps - 1) / kWarps : 0;
 
-    // ---- bulk copies of this warp's k-th tile of the item
+    // ---- copies of this warp's k-th tile of the item
     const int64_t head_codes = static_cast<int64_t>(h) * c.page_size * (D / 2);
     const int64_t head_scales = static_cast<int64_t>(h) * c.page_size * (D / 16);
     const int* const row_table = p.a.table + b * p.a.table_stride;
@@ -826,7 +839,7 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   p.join = join_ctas < num_sms ? Plan::kByRow : (join_ctas <= 512 ? Plan::kByTile : Plan::kListed);
   const double tiles = static_cast<double>(batch) * p.items * static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
   p.fits = tiles < 0x7FF00000;
-  const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(p.nt);
+  const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(head_dim, p.nt);
   const double want = tiles / kWarps + 1.0;
   p.ctas = static_cast<int>(want < static_cast<double>(wave) ? static_cast<int64_t>(want) : wave);
   p.rows_bytes = (static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (head_dim + 2) * sizeof(float) +

@@ -34,8 +34,7 @@ cudaError_t launch_kv_read(const nvfp4_kv_cache& c, int64_t tokens, const int64_
                            void* K, void* V, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_copy_pages(const nvfp4_kv_cache& c, int64_t layers,
                                  int64_t code_layer_stride, int64_t scale_layer_stride,
-                                 const int* src, const int* dst, int64_t n, int num_sms,
-                                 cudaStream_t stream);
+                                 const int* src, const int* dst, int64_t n, cudaStream_t stream);
 
 // One attention call, checked by the entry point.
 struct KvAttention {

@@ -133,11 +133,9 @@ int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t cod
   } catch (...) {
     return NVFP4_ERR_INVALID_ARG;
   }
-  const int sms = nvfp4::sm_count();
-  if (sms <= 0) return nvfp4::record_cuda_status(cudaErrorNoDevice);
   return nvfp4::record_cuda_status(nvfp4::launch_kv_copy_pages(
       *cache, layers, layers > 1 ? code_layer_stride : 0, layers > 1 ? scale_layer_stride : 0, src,
-      dst, n, sms, static_cast<cudaStream_t>(stream)));
+      dst, n, static_cast<cudaStream_t>(stream)));
 }
 
 size_t nvfp4_kv_attention_workspace_size(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
