@@ -260,7 +260,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
   const int first = all_first + begin;
   const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (split + 1) / p.splits) - begin;
 
-  const int tiles = rows - r0 > kTileRows ? 2 : 1;  // with rows in them
+  // steps [from(t), to(t)) of them in which tile t sees a token: with a window
+  // or causally the other steps are the other tile's only
+  int tile_from[2], tile_to[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int a = r0 + t * kTileRows, z = min(a + kTileRows, rows) - 1;
+    int t_lo, t_hi, other;
+    visible(p, s, a, t_lo, other);
+    visible(p, s, z, other, t_hi);
+    const bool some = a <= z && t_hi > t_lo;
+    tile_from[t] = some ? min(max(t_lo / kTokens - first, 0), steps) : 0;
+    tile_to[t] = some ? min(max((t_hi + kTokens - 1) / kTokens - first, tile_from[t]), steps) : 0;
+  }
   auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -339,15 +351,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       const int tok = (first + i) * kTokens + 16 * lane;
       return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : 0;
     };
-    int page = page_of(0);
+    int page = 0;
     float m = -INFINITY, down = 0.0f, l = 0.0f;
-    const int my_steps = t < tiles ? steps : 0;
-    for (int i = 0; i < my_steps; ++i) {
+    const int from = t ? tile_from[1] : tile_from[0], to = t ? tile_to[1] : tile_to[0];
+    page = page_of(from);
+    for (int i = from; i < to; ++i) {
+      const uint32_t parity = (i - from) & 1;
       const int tb = (first + i) * kTokens;
       const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
       page = page_of(i + 1);
       const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
-      mbar_wait<kSoftmaxSleep>(&sh, bar(kSFull + t), i & 1);
+      mbar_wait<kSoftmaxSleep>(&sh, bar(kSFull + t), parity);
       tc_fence_after();
       uint32_t x[4][32];
 #pragma unroll
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         m = top;
         down = top == -INFINITY ? 0.0f : -top;
         l *= r;
-        if (i > 0) {
+        if (i > from) {
 #pragma unroll 1
           for (int q = 0; q < D / 16; ++q) {
             uint32_t o[16];
@@ -436,7 +450,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       mbar_arrive(bar(kPFull + 2 * t + 1));
     }
     // -------------------------------------------------------------- result
-    if (my_steps > 0) {
+    if (to > from) {
       mbar_wait(&sh, bar(kOFull + t), 0);
       tc_fence_after();
       mbar_wait(&sh, bar(kScan), 0);
@@ -462,7 +476,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       uint32_t x[32];
-      if (my_steps > 0) {
+      if (to > from) {
         tmem_load32(o_col + 32 * q, x);
         tmem_wait_load();
       } else {
@@ -631,16 +645,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int k = k0; k < k1; ++k)
           mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, v0 + k * (2048 >> 4), kPv, add || k > 0);
       };
+      auto active = [&](int t, int i) {
+        return t ? i >= tile_from[1] && i < tile_to[1] : i >= tile_from[0] && i < tile_to[0];
+      };
       mbar_wait(&sh, bar(kKFull), 0);
-      for (int t = 0; t < tiles; ++t) {
-        mbar_wait(&sh, bar(kQFull + t), 0);
-        tc_fence_after();
-        if (elect_one()) {
-          qk(t, 0);
-          if (t == tiles - 1) tc_commit(bar(kKEmpty));
-        }
-        __syncwarp();
+      mbar_wait(&sh, bar(kQFull), 0);
+      mbar_wait(&sh, bar(kQFull + 1), 0);
+      tc_fence_after();
+      if (elect_one()) {
+        for (int t = 0; t < 2; ++t)
+          if (active(t, 0)) qk(t, 0);
+        tc_commit(bar(kKEmpty));
       }
+      __syncwarp();
       // One warp issues for both tiles, in turn: with a warp each their MMAs
       // mix and both tiles wait for both (631 us instead of 502 for 4 x 2048
       // rows over 8192).
@@ -649,20 +666,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         const bool more = i + 1 < steps;
         mbar_wait(&sh, bar(kVFull + st), (i >> 1) & 1);
         if (more) mbar_wait(&sh, bar(kKFull + nst), ((i + 1) >> 1) & 1);
-        for (int t = 0; t < tiles; ++t) {
-          mbar_wait(&sh, bar(kPFull + 2 * t), i & 1);
-          tc_fence_after();
-          if (elect_one()) pv(t, st, 0, kTokens / 32, i > 0);
-          __syncwarp();
-          mbar_wait(&sh, bar(kPFull + 2 * t + 1), i & 1);
-          tc_fence_after();
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+          const bool now = active(t, i), next = more && active(t, i + 1);
+          const int from = t ? tile_from[1] : tile_from[0];
+          if (now) {
+            const uint32_t parity = (i - from) & 1;
+            mbar_wait(&sh, bar(kPFull + 2 * t), parity);
+            tc_fence_after();
+            if (elect_one()) pv(t, st, 0, kTokens / 32, i > from);
+            __syncwarp();
+            mbar_wait(&sh, bar(kPFull + 2 * t + 1), parity);
+            tc_fence_after();
+          }
           if (elect_one()) {
-            pv(t, st, kTokens / 32, kTokens / 16, true);
-            if (more)
-              qk(t, nst);
-            else
-              tc_commit(bar(kOFull + t));
-            if (t == tiles - 1) {
+            if (now) pv(t, st, kTokens / 32, kTokens / 16, true);
+            if (now && !next) tc_commit(bar(kOFull + t));
+            if (next) qk(t, nst);
+            if (t == 1) {
               tc_commit(bar(kVEmpty + st));
               if (more) tc_commit(bar(kKEmpty + nst));
             }
@@ -671,9 +692,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         }
       }
       // nothing of this CTA's is in flight when it ends
-      for (int t = 0; t < tiles; ++t) {
-        mbar_wait(&sh, bar(kOFull + t), 0);
-        mbar_drain(bar(kOFull + t), 0);
+      for (int t = 0; t < 2; ++t) {
+        if (t ? tile_to[1] > tile_from[1] : tile_to[0] > tile_from[0]) {
+          mbar_wait(&sh, bar(kOFull + t), 0);
+          mbar_drain(bar(kOFull + t), 0);
+        }
       }
     }
   }
