@@ -695,8 +695,9 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 // A CTA for RC rows of an item (8, or 1 where there are few items): adds up the
 // partial results of an item that was cut, in an order that depends on their
 // number alone.  The items are all of the call's, whose pieces each CTA works
-// out while kv_rows_kernel still runs, or (kList) those that it listed as cut.  D / 4 lanes take 4 elements each of the rows of a piece, the
-// CTA's 8 warps every kStripes-th piece.
+// out while kv_rows_kernel still runs, or (kList) those that it listed as cut.
+// D / 4 lanes take 4 elements each of the rows of a piece, the CTA's 8 warps
+// every kStripes-th piece.
 constexpr int kJoinWarps = 8;
 
 template <int D, int NT, int RC, bool kList>
