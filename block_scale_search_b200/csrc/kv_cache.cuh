@@ -24,8 +24,17 @@ struct KvRows {  // strided rows [token][head][dim] of K or V, strides in elemen
   int64_t token_stride, head_stride;
 };
 
-// SM count of the current device, cached (0 on failure).
-int sm_count();
+// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
+// low half of r[i].
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
 
 cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvRows& V, int type,
                              int64_t tokens, const int64_t* slots, int* status, int num_sms,

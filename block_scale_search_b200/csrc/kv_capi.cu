@@ -2,6 +2,7 @@
 // everywhere: arguments are checked on the host before anything is enqueued,
 // and no C++ exception leaves.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -19,6 +20,23 @@ namespace {
 constexpr int64_t kIntMax = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxStride = int64_t{1} << 40;  // guards index arithmetic
 constexpr int64_t kMaxPageStride = (int64_t{1} << 32) - 16;
+
+// SM count of the current device, cached per device ordinal (0 on failure).
+int sm_count() {
+  static std::atomic<int> cache[128];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 128 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 128) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -80,7 +98,7 @@ int nvfp4_kv_append(const nvfp4_kv_cache* cache, const void* K, const void* V, i
   if ((st = check_rows(V, v_token_stride, v_head_stride, size)) != NVFP4_OK) return st;
   if (!aligned(slots, 8) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
   if (tokens == 0 && status == nullptr) return NVFP4_OK;
-  const int sms = nvfp4::sm_count();
+  const int sms = sm_count();
   if (sms <= 0) return nvfp4::record_cuda_status(cudaErrorNoDevice);
   return nvfp4::record_cuda_status(nvfp4::launch_kv_append(
       *cache, nvfp4::KvRows{K, k_token_stride, k_head_stride},
@@ -98,7 +116,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
   if (tokens > kMaxStride) return NVFP4_ERR_SHAPE;
   if (!aligned(K, 32) || !aligned(V, 32) || !aligned(slots, 8)) return NVFP4_ERR_ALIGN;
   if (tokens == 0) return NVFP4_OK;
-  const int sms = nvfp4::sm_count();
+  const int sms = sm_count();
   if (sms <= 0) return nvfp4::record_cuda_status(cudaErrorNoDevice);
   return nvfp4::record_cuda_status(nvfp4::launch_kv_read(*cache, tokens, slots, type, K, V, sms,
                                                          static_cast<cudaStream_t>(stream)));
@@ -141,7 +159,7 @@ int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t cod
 size_t nvfp4_kv_attention_workspace_size(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                          int kv_heads, int head_dim) {
   if (check_attention_sizes(batch, max_q, max_kv, q_heads, kv_heads, head_dim) != NVFP4_OK) return 0;
-  const int sms = nvfp4::sm_count();
+  const int sms = sm_count();
   if (sms <= 0) return 0;
   return nvfp4::kv_attention_workspace_bytes(batch, max_q, max_kv, q_heads, kv_heads, head_dim, sms);
 }
@@ -176,7 +194,7 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* Q, int type, int
   if (empty) return NVFP4_OK;
   if (workspace == nullptr) return NVFP4_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
-  const int sms = nvfp4::sm_count();
+  const int sms = sm_count();
   if (sms <= 0) return nvfp4::record_cuda_status(cudaErrorNoDevice);
   const size_t need =
       nvfp4::kv_attention_workspace_bytes(batch, max_q, max_kv, q_heads, cache->kv_heads, cache->head_dim, sms);

@@ -52,18 +52,6 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
   return r;
 }
 
-// The eight E2M1 values of a word as four f16x2, byte i's low nibble in the
-// low half of r[i].
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
-  asm("{ .reg .b8 a, b, c, d;\n"
-      "mov.b32 {a, b, c, d}, %4;\n"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
-      "cvt.rn.f16x2.e2m1x2 %3, d; }"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
-}
-
 // Round x >= 0 to the E2M1 grid {0,.5,1,1.5,2,3,4,6} with ties to the even
 // code and saturation at 6, using only the FP pipes: on [2^e, 2^(e+1)) the grid
 // step is 2^(e-1) (e >= 0) and 0.5 below 1, so adding and subtracting

@@ -131,7 +131,6 @@ int resident_ctas(const void* kernel, int threads_per_cta) {
 
 namespace nvfp4 {
 int record_cuda_status(cudaError_t e) { return cuda_status(e); }
-int sm_count() { return current_sm_count(); }
 
 // The checked build's per-translation-unit records (checks.cuh).
 namespace {
