@@ -3,8 +3,8 @@
 // All three are bound by HBM: append reads 2 (or 4) bytes an element and
 // writes 0.5625, read the reverse, copy moves bytes.  Measured with 8 heads of
 // 128: append of 16001 tokens 24 us (3.5 TB/s; 220 instructions a group of 16
-// keep the schedulers 60% busy beside it), read of 100003 tokens to FP16 96 us
-// (5.4 TB/s), copy of 511 pages in 16 layers 99 us (6.1 TB/s).
+// keep the schedulers 60% busy beside it), read of 100003 tokens to FP16 88 us
+// (6.0 TB/s), copy of 511 pages in 16 layers 99 us (6.1 TB/s).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -210,10 +210,15 @@ __device__ __forceinline__ bool locate(const nvfp4_kv_cache& c, int page_shift, 
   return true;
 }
 
-constexpr int kAppendUnroll = 2, kReadUnroll = 4;  // tokens whose loads are in flight per thread
+// Tokens whose loads are in flight per thread, and resident CTAs an SM, which
+// are as many as are launched (two waves of 4 with 4 tokens: 100003 tokens read
+// in 96 us, one wave 93, 3 with 8 tokens 88, 2 with 16 88 but 500 tokens 3.5
+// instead of 2.7; append of 16001 with 4 tokens and 2 CTAs 1 us more).
+constexpr int kAppendUnroll = 2, kReadUnroll = 8;
+constexpr int kAppendCtas = 4, kReadCtas = 3;
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kAppendCtas)
 kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens,
                  const int64_t* __restrict__ slots, int* __restrict__ status) {
   for_groups<kAppendUnroll>(c, m, tokens, [&](const int64_t(&ts)[kAppendUnroll], bool isv, uint32_t h, uint32_t g) {
@@ -247,14 +252,16 @@ kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens
 
 // -------------------------------------------------------------------- read
 
+// (evict first: what is read back is written once, and should not push the
+// cache's pages out of L2; append of 16001 tokens and their read back 47 -> 44 us)
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+  asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kReadCtas)
 kv_read_kernel(nvfp4_kv_cache c, Columns m, int64_t tokens, const int64_t* __restrict__ slots, void* __restrict__ K,
                void* __restrict__ V) {
   constexpr int kSize = kType == kFp32 ? 4 : 2;
@@ -371,14 +378,14 @@ struct TokenGrid {
   Columns m;
   unsigned blocks;
 };
-// One wave of CTAs at most, 8 an SM.
-TokenGrid token_grid(const nvfp4_kv_cache& c, int64_t tokens, int num_sms) {
+// One wave of resident CTAs at most.
+TokenGrid token_grid(const nvfp4_kv_cache& c, int64_t tokens, int num_sms, int ctas_per_sm) {
   TokenGrid g{};
   g.m.per_token = 2u * c.kv_heads * (c.head_dim / 16);
   g.m.per_pass = g.m.per_token <= kThreads ? kThreads / g.m.per_token : 1;
   while ((1 << g.m.page_shift) < c.page_size) ++g.m.page_shift;
   int64_t blocks = (tokens + g.m.per_pass - 1) / g.m.per_pass;
-  const int64_t wave = static_cast<int64_t>(num_sms) * 8;
+  const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm;
   if (blocks > wave) blocks = wave;
   g.blocks = static_cast<unsigned>(blocks);
   return g;
@@ -394,7 +401,7 @@ cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvR
     if (e != cudaSuccess) return e;
   }
   if (tokens == 0) return cudaSuccess;
-  const TokenGrid g = token_grid(c, tokens, num_sms);
+  const TokenGrid g = token_grid(c, tokens, num_sms, kAppendCtas);
   auto launch = [&](auto t) {
     kv_append_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, K, V, g.m, tokens, slots, status);
   };
@@ -407,7 +414,7 @@ cudaError_t launch_kv_append(const nvfp4_kv_cache& c, const KvRows& K, const KvR
 cudaError_t launch_kv_read(const nvfp4_kv_cache& c, int64_t tokens, const int64_t* slots, int type,
                            void* K, void* V, int num_sms, cudaStream_t stream) {
   if (tokens == 0) return cudaSuccess;
-  const TokenGrid g = token_grid(c, tokens, num_sms);
+  const TokenGrid g = token_grid(c, tokens, num_sms, kReadCtas);
   auto launch = [&](auto t) {
     kv_read_kernel<decltype(t)::value><<<g.blocks, kThreads, 0, stream>>>(c, g.m, tokens, slots, K, V);
   };
