@@ -10,6 +10,7 @@ library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import threading
 
@@ -201,12 +202,14 @@ def _check(fn: str, st: int):
 
 
 def _ptr(t) -> int | None:
-    if t is None or isinstance(t, int):
-        return t
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> int | None:
+    if type(stream) is int:
+        return stream
     if stream is None:
         # the handle without a Stream object around it (3 us less)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -949,7 +952,8 @@ def _one_layer(cache):
 
 
 def _kv_rows(t, name, heads, dim, device, types):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype not in types or t.device != device:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.dtype not in types or t.device != device:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}] on the cache's device, of a supported type")
     if t.stride(2) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
@@ -964,17 +968,24 @@ def _int_vector(t, name, kind, device, n=None):
 
 
 def _on(call, device, stream):
-    """call() with the device current, and with a given stream current for what
-    it allocates (so that the allocator knows where that is used)."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call()
+    """call(handle of the stream) with the device current, and with a given stream
+    current for what it allocates (so that the allocator knows where that is used)."""
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device):
         if stream is None:
-            return call()
+            return call(torch._C._cuda_getCurrentRawStream(index))
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
-            return call()
+            return call(stream.cuda_stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_workspace_bytes(device_index, *sizes):
+    """nvfp4_kv_attention_workspace_size on that device, which is current."""
+    return nvfp4_kv_attention_workspace_size(*sizes)
 
 
 def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
@@ -992,8 +1003,10 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
     _int_vector(slots, "slots", torch.int64, cache.device, n)
     if status is not None:
         _int_vector(status, "status", torch.int32, cache.device, 1)
-    _on(lambda: nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, K.stride(0), K.stride(1), V.stride(0), V.stride(1),
-                                slots, status), cache.device, stream)
+    k0, k1, _ = K.stride()
+    v0, v1, _ = V.stride()
+    _on(lambda handle: nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, k0, k1, v0, v1, slots, status, handle),
+        cache.device, stream)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, out=None, stream=None):
@@ -1009,12 +1022,12 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
         if not (K.is_contiguous() and V.is_contiguous() and K.shape[0] == V.shape[0] == n):
             raise ValueError("out must be two contiguous tensors with a row for every slot")
 
-    def call():
+    def call(handle):
         if out is not None:
             k, v = out
         else:
             k, v = torch.empty(2, n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device).unbind(0)
-        nvfp4_kv_read(d, slots, n, _TYPES[dtype], k, v)
+        nvfp4_kv_read(d, slots, n, _TYPES[dtype], k, v, handle)
         return k, v
 
     return _on(call, cache.device, stream)
@@ -1029,8 +1042,8 @@ def kv_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be lists of as many pages")
     many = cache.k_codes.dim() == 5
-    _on(lambda: nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
-                                    cache.k_scales.stride(0) if many else 0, src, dst, src.numel()),
+    _on(lambda handle: nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
+                                           cache.k_scales.stride(0) if many else 0, src, dst, src.numel(), handle),
         cache.device, stream)
 
 
@@ -1048,38 +1061,44 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
     dev = cache.device
     if Q.dim() != 3:
         raise ValueError("Q must be [total, q_heads, head_dim]")
-    heads = Q.shape[1]
-    _kv_rows(Q, "Q", heads, d.head_dim, dev, (torch.bfloat16, torch.float16))
+    total, heads, _ = Q.shape
+    dim = d.head_dim
+    _kv_rows(Q, "Q", heads, dim, dev, (torch.bfloat16, torch.float16))
     _int_vector(kv_lengths, "kv_lengths", torch.int32, dev)
-    batch, total = kv_lengths.numel(), Q.shape[0]
+    batch = kv_lengths.shape[0]
     _int_vector(q_offsets, "q_offsets", torch.int32, dev, batch + 1)
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev
-            or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1)
-            or (batch > 1 and page_table.stride(0) < page_table.shape[1])):
-        raise ValueError("page_table must be int32 [batch, pages], rows contiguous, on the cache's device")
-    if max_kv > page_table.shape[1] * d.page_size:
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != dev:
+        raise ValueError("page_table must be int32 [batch, pages], on the cache's device")
+    n, pages = page_table.shape
+    table_stride, inner = page_table.stride()
+    if n != batch or (pages > 1 and inner != 1) or (batch > 1 and table_stride < pages):
+        raise ValueError("page_table must have a row for every sequence, rows contiguous")
+    if max_kv > pages * d.page_size:
         raise ValueError("max_kv is more than the page table's rows hold")
     if out is not None:
-        _kv_rows(out, "out", heads, d.head_dim, dev, (Q.dtype,))
+        _kv_rows(out, "out", heads, dim, dev, (Q.dtype,))
         if out.shape[0] != total:
             raise ValueError("out must have Q's rows")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads) or lse.device != dev
                             or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [total, q_heads]")
 
-    def call():
+    def call(handle):
         o = torch.empty_like(Q) if out is None else out
         z = torch.empty(total, heads, dtype=torch.float32, device=dev) if lse is None and want_lse else lse
-        ws = workspace
-        if ws is None and batch and total and max_q > 0:
-            nb = nvfp4_kv_attention_workspace_size(batch, max_q, max_kv, heads, d.kv_heads, d.head_dim)
+        ws, nb = workspace, 0
+        if ws is not None:
+            nb = ws.numel() * ws.element_size()
+        elif batch and total and max_q > 0:
+            nb = _kv_workspace_bytes(dev.index, batch, max_q, max_kv, heads, d.kv_heads, dim)
             if nb == 0:
                 raise NVFP4Error("nvfp4_kv_attention_workspace_size", -1)
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, Q.stride(0), Q.stride(1), q_offsets, kv_lengths,
-                           page_table, max(page_table.stride(0), page_table.shape[1]), batch, max_q, max_kv,
-                           d.head_dim ** -0.5 if sm_scale is None else sm_scale, causal, window, o, o.stride(0),
-                           o.stride(1), z, ws, ws.numel() * ws.element_size() if ws is not None else 0)
+        q0, q1, _ = Q.stride()
+        o0, o1, _ = o.stride()
+        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, q0, q1, q_offsets, kv_lengths, page_table,
+                           max(table_stride, pages), batch, max_q, max_kv, dim ** -0.5 if sm_scale is None else sm_scale,
+                           causal, window, o, o0, o1, z, ws, nb, handle)
         return o if z is None else (o, z)
 
     return _on(call, dev, stream)
