@@ -1082,6 +1082,8 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads) or lse.device != dev
                             or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [total, q_heads]")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous, on the cache's device")
 
     def call(handle):
         o = torch.empty_like(Q) if out is None else out

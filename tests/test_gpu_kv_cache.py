@@ -816,3 +816,16 @@ def test_work_beyond_32_bits_is_refused(nv):
         nv.nvfp4_kv_attention(cache.desc, z, 0, 64, 8, 8192, 128, z, z, z, 1 << 16, 60000, 1, 1 << 20, 0.1, 1, 0, z,
                               8192, 128, None, torch.empty(1 << 12, dtype=torch.uint8, device=DEV), 1 << 40)
     assert e.value.status == -2
+
+
+def test_workspace_elsewhere_is_refused(nv):
+    gen = torch.Generator().manual_seed(18)
+    cache = make_cache(nv, gen, 4, 16, 2, 64)
+    Q = torch.zeros(1, 4, 64, dtype=BF16, device=DEV)
+    off, lens = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 1], [20]))
+    table = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    n = nv.nvfp4_kv_attention_workspace_size(1, 1, 20, 4, 2, 64)
+    nv.kv_attention(cache, Q, off, lens, table, 1, 20, workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            nv.kv_attention(cache, Q, off, lens, table, 1, 20, workspace=ws)
