@@ -888,23 +888,26 @@ class KVCache:
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_S, v_S):
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_S, self.v_S = k_S, v_S
-        shape, small = k_codes.shape, k_scales.shape
-        if len(shape) not in (4, 5):
+        shape, stride = k_codes.shape, k_codes.stride()
+        if len(shape) == 4:
+            pages, h, p, half = shape
+            page_stride, s1, s2, s3 = stride
+            lead, s_shape, self.layers = (), (h,), 1
+        elif len(shape) == 5:
+            layers, pages, h, p, half = shape
+            _, page_stride, s1, s2, s3 = stride
+            lead, s_shape, self.layers = (layers,), (layers, h), layers
+        else:
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim/2], or that after layers")
-        pages, h, p, half = shape[-4:]
-        dim = 2 * half
-        if small[:-1] != shape[:-1] or 16 * small[-1] != dim or v_codes.shape != shape or v_scales.shape != small:
+        dim, groups = 2 * half, half // 8
+        small = (*lead, pages, h, p, groups)
+        if half % 8 or v_codes.shape != shape or k_scales.shape != small or v_scales.shape != small:
             raise ValueError("codes and scales of K and V must agree in shape")
-        stride, small_stride = k_codes.stride(), k_scales.stride()
+        small_stride = k_scales.stride()
         if v_codes.stride() != stride or v_scales.stride() != small_stride:
             raise ValueError("K and V must have the same strides")
-        if stride[-3:] != (p * half, half, 1) or small_stride[-3:] != (p * dim // 16, dim // 16, 1):
+        if s3 != 1 or s2 != half or s1 != p * half or small_stride[-3:] != (p * groups, groups, 1):
             raise ValueError("a page must be contiguous")
-        s_shape = (h,)
-        self.layers = 1
-        if len(shape) == 5:
-            self.layers = shape[0]
-            s_shape = (shape[0], h)
         self.device = k_codes.device
         where = k_codes.get_device()  # -1 on the CPU
         u8, f32 = torch.uint8, torch.float32
@@ -917,7 +920,7 @@ class KVCache:
             raise ValueError("S must be contiguous [kv_heads], or [layers, kv_heads]")
         self.desc = KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                 v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), pages,
-                                stride[-4], small_stride[-4], p, h, dim)
+                                page_stride, small_stride[-4], p, h, dim)
 
     @classmethod
     def empty(cls, pages, page_size, kv_heads, head_dim, k_S, v_S, layers=None):
@@ -1005,7 +1008,9 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
         _int_vector(status, "status", torch.int32, cache.device, 1)
     k0, k1, _ = K.stride()
     v0, v1, _ = V.stride()
-    _on(lambda handle: nvfp4_kv_append(d, K, V, _TYPES[K.dtype], n, k0, k1, v0, v1, slots, status, handle),
+    kind = _TYPES[K.dtype]
+    _on(lambda handle: _check("nvfp4_kv_append", lib().nvfp4_kv_append(
+        C.byref(d), K.data_ptr(), V.data_ptr(), kind, n, k0, k1, v0, v1, slots.data_ptr(), _ptr(status), handle)),
         cache.device, stream)
 
 
@@ -1027,7 +1032,8 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
             k, v = out
         else:
             k, v = torch.empty(2, n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device).unbind(0)
-        nvfp4_kv_read(d, slots, n, _TYPES[dtype], k, v, handle)
+        _check("nvfp4_kv_read", lib().nvfp4_kv_read(C.byref(d), slots.data_ptr(), n, _TYPES[dtype], k.data_ptr(),
+                                                    v.data_ptr(), handle))
         return k, v
 
     return _on(call, cache.device, stream)
@@ -1098,9 +1104,11 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         q0, q1, _ = Q.stride()
         o0, o1, _ = o.stride()
-        nvfp4_kv_attention(d, Q, _TYPES[Q.dtype], heads, total, q0, q1, q_offsets, kv_lengths, page_table,
-                           max(table_stride, pages), batch, max_q, max_kv, dim ** -0.5 if sm_scale is None else sm_scale,
-                           causal, window, o, o0, o1, z, ws, nb, handle)
+        _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
+            C.byref(d), Q.data_ptr(), _TYPES[Q.dtype], heads, total, q0, q1, q_offsets.data_ptr(),
+            kv_lengths.data_ptr(), page_table.data_ptr(), max(table_stride, pages), batch, max_q, max_kv,
+            dim ** -0.5 if sm_scale is None else float(sm_scale), int(causal), window, o.data_ptr(), o0, o1, _ptr(z),
+            _ptr(ws), nb, handle))
         return o if z is None else (o, z)
 
     return _on(call, dev, stream)
