@@ -829,3 +829,28 @@ def test_workspace_elsewhere_is_refused(nv):
     for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
         with pytest.raises(ValueError):
             nv.kv_attention(cache, Q, off, lens, table, 1, 20, workspace=ws)
+
+
+@pytest.mark.parametrize("dim,heads,n", [(128, 8, 9001), (16, 1, 120003), (240, 5, 3333), (64, 40, 5002)])
+def test_many_tokens_equal_few(nv, dim, heads, n):
+    """Calls whose threads take several tokens each, against calls of a few hundred."""
+    gen = torch.Generator().manual_seed(n)
+    pages = n // 16 + 3
+    S = torch.rand(heads, generator=gen).to(DEV) * 1e-3 + 1e-4
+    one, few = (nv.KVCache.empty(pages, 16, heads, dim, S, S.flip(0)) for _ in range(2))
+    K, V = (torch.randn(n, heads, dim, generator=gen).bfloat16().to(DEV) for _ in range(2))
+    slots = torch.randperm(pages * 16, generator=gen)[:n]
+    slots[::97] = -1
+    slots = slots.to(DEV)
+    status = torch.ones(1, dtype=torch.int32, device=DEV)
+    nv.kv_append(one, K, V, slots, status)
+    for a in range(0, n, 301):
+        nv.kv_append(few, K[a:a + 301], V[a:a + 301], slots[a:a + 301])
+    assert int(status) == 0
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(one, name), getattr(few, name)), name
+    for kind in (BF16, FP32):
+        k, v = nv.kv_read(one, slots, kind)
+        for a in range(0, n, 301):
+            k1, v1 = nv.kv_read(one, slots[a:a + 301], kind)
+            assert torch.equal(k[a:a + 301], k1) and torch.equal(v[a:a + 301], v1), a
