@@ -54,7 +54,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;    // tokens a warp takes at a time, in two halves of 16
 constexpr int kHalf = kTile / 2;
-constexpr int kStages = 2;   // tiles of a warp's ring
+constexpr int kStages = 2;   // tiles of a warp's ring (and the code below counts on 2)
 // What starting and finishing an item costs a CTA, in tiles: its page ids and
 // queries arrive in two trips to memory, its warps meet twice at the end.
 constexpr int kItemCost = 10;
@@ -309,9 +309,10 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       if (k >= mine || tok >= s.lk) return -1;
       return row_table[tok >> p.page_shift];  // (looked at when it is used: a look waits for the load)
     };
-    // lane i: pages of tile ids_base + i
-    int ids0 = page_at(lane, 0), ids1 = page_at(lane, 1), ids_base = 0;
-    uint32_t dead = 0;  // bits 2 (tile % 16), + 1: no page there (zeros are written)
+    // lane i: pages of tile i of the 32 that are next
+    int ids0 = page_at(lane, 0), ids1 = page_at(lane, 1);
+    uint32_t bad0 = 0, bad1 = 0;  // bit i: no page there (zeros are written)
+    uint32_t none_next = 0;       // of the tile requested last: bit `half`, no page
     int requested = 0;
     // The queries' loads go out before the tiles': behind them they would wait
     // for the whole GPU's first requests to be served.  A thread takes 8
@@ -349,21 +350,24 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     int fill = 0;  // ring position of the next request, in bytes
     auto request = [&]() {
       if (requested < mine) {
-        if (requested == ids_base + 32) {
-          ids_base += 32;
-          ids0 = page_at(ids_base + lane, 0);
-          ids1 = page_at(ids_base + lane, 1);
+        const int at = requested & 31;
+        if (at == 0) {  // the first use of 32 ids
+          if (requested > 0) {
+            ids0 = page_at(requested + lane, 0);
+            ids1 = page_at(requested + lane, 1);
+          }
+          const bool ok0 = ids0 >= 0 && ids0 < c.num_pages, ok1 = ids1 >= 0 && ids1 < c.num_pages;
+          bad0 = __ballot_sync(0xFFFFFFFFu, !ok0);
+          bad1 = __ballot_sync(0xFFFFFFFFu, !ok1);
+          ids0 = ok0 ? ids0 : 0;
+          ids1 = ok1 ? ids1 : 0;
         }
-        const int id0 = __shfl_sync(0xFFFFFFFFu, ids0, requested - ids_base);
-        const int id1 = __shfl_sync(0xFFFFFFFFu, ids1, requested - ids_base);
-        const bool ok0 = id0 >= 0 && id0 < c.num_pages, ok1 = id1 >= 0 && id1 < c.num_pages;
-        const uint32_t none = (ok0 ? 0u : 1u) | (ok1 ? 0u : 2u);
-        const int sh = 2 * (requested & 15);
-        dead = (dead & ~(3u << sh)) | (none << sh);
+        const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, ids0, at), p1 = __shfl_sync(0xFFFFFFFFu, ids1, at);
+        const uint32_t no0 = (bad0 >> at) & 1u, no1 = (bad1 >> at) & 1u;
+        none_next = no0 + 2 * no1;
+        const int n0 = 16 - 16 * no0, n1 = 16 - 16 * no1;
         const uint32_t row0 = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
         const uint32_t row1 = (row0 + kHalf) & (c.page_size - 1);
-        const int n0 = ok0 ? 16 : 0, n1 = ok1 ? 16 : 0;
-        const uint32_t p0 = ok0 ? id0 : 0, p1 = ok1 ? id1 : 0;
         const uint64_t off0 = static_cast<uint64_t>(p0) * code_page + row0 * (D / 2);
         const uint64_t off1 = static_cast<uint64_t>(p1) * code_page + row1 * (D / 2);
         const uint32_t dst = code_dst + fill;
@@ -383,7 +387,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
           copy16<0, 0>(sc_dst + fill, sc_src + off, second ? n1 : n0);
         }
         ++requested;
-        fill = fill == (kStages - 1) * kStageBytes ? 0 : fill + kStageBytes;
+        fill = kStageBytes - fill;
       }
       copy_commit();
     };
@@ -450,13 +454,13 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 
     int use = 0;  // ring position of the tile in use, in bytes
     for (int k = 0; k < mine; ++k) {
+      const uint32_t none = none_next;
       request();
       copy_wait<kStages - 1>();
       __syncwarp();
       const uint8_t* const stage = ring + use;
-      use = use == (kStages - 1) * kStageBytes ? 0 : use + kStageBytes;
+      use = kStageBytes - use;
       const int tb = (s.t0 + ts + warp + k * kWarps) * kTile;  // first token
-      const uint32_t none = (dead >> (2 * (k & 15))) & 3u;
       const bool edge = tb < all_lo || tb + kTile > all_hi || none != 0;
       // ---- S^T
       float x[NT][2][4] = {};
