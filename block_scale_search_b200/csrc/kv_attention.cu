@@ -26,14 +26,15 @@
 //     the rounding of a 16-bit result); sums and the running maximum are FP32.
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
-// A tile of 32 tokens takes 670 instructions at head_dim 128 with 8 rows, 128
+// A tile of 32 tokens takes 680 instructions at head_dim 128 with 8 rows, 140
 // of them conversions, 128 products with scales and 32 MMAs (2, 2 and 8.5
 // cycles of a scheduler each), against 745 cycles of a scheduler's share of
-// HBM; in the loop it takes about 780, that is 6.3 TB/s.  Over a whole call
-// 4.1 TB/s (48 sequences of up to 8192 tokens, 64 / 8 heads of 128: 60 us) and
-// 4.5 TB/s (two of 131072: 67 us) remain: a CTA takes about 6 us until its
-// first tile is there (lengths, page ids and tiles are three trips to memory
-// one after another) and 2 us to join its warps, the cut items 3 to 5 us.
+// HBM; in the loop it takes about 900, that is 5.7 TB/s, also where the cache
+// lies in L2: what bounds it is instructions.  Over a whole call 4.2 TB/s (48
+// sequences of up to 8192 tokens, 64 / 8 heads of 128: 58.6 us) and 4.7 TB/s
+// (two of 131072: 65.0 us) remain: a CTA takes about 6 us until its first tile
+// is there (lengths, page ids and tiles are three trips to memory one after
+// another) and 2 us to join its warps, the cut items 3 to 5 us.
 //
 // Work split: the tiles (32 tokens) of all (sequence, row block, KV head)
 // items form one line; each CTA takes an equal piece of it, cutting items
