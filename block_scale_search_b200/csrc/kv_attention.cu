@@ -97,6 +97,13 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
+// a where `mask` is 1 and b where it is 0, in one instruction (the compiler
+// rewrites the C expression with shifts into two)
+__device__ __forceinline__ uint32_t merge(uint32_t a, uint32_t b, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(mask));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -598,10 +605,10 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         for (int w = 0; w < VW; ++w) {
           constexpr uint32_t kLow = 0x0F0F0F0Fu;
           uint32_t lo_ab[4], hi_ab[4], lo_cd[4], hi_cd[4];
-          e2m1x8_to_f16x2((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), lo_ab);
-          e2m1x8_to_f16x2(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), hi_ab);
-          e2m1x8_to_f16x2((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), lo_cd);
-          e2m1x8_to_f16x2(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), hi_cd);
+          e2m1x8_to_f16x2(merge(vw[0][w], vw[1][w] << 4, kLow), lo_ab);
+          e2m1x8_to_f16x2(merge(vw[0][w] >> 4, vw[1][w], kLow), hi_ab);
+          e2m1x8_to_f16x2(merge(vw[2][w], vw[3][w] << 4, kLow), lo_cd);
+          e2m1x8_to_f16x2(merge(vw[2][w] >> 4, vw[3][w], kLow), hi_cd);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint32_t a[4] = {mul_f16x2(lo_ab[u], sab), mul_f16x2(hi_ab[u], sab),
