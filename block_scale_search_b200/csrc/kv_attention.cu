@@ -26,13 +26,13 @@
 //     the rounding of a 16-bit result); sums and the running maximum are FP32.
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
-// A tile of 32 tokens takes 680 instructions at head_dim 128 with 8 rows, 140
+// A tile of 32 tokens takes 640 instructions at head_dim 128 with 8 rows, 140
 // of them conversions, 128 products with scales and 32 MMAs (2, 2 and 8.5
 // cycles of a scheduler each), against 745 cycles of a scheduler's share of
-// HBM; in the loop it takes about 900, that is 5.7 TB/s, also where the cache
-// lies in L2: what bounds it is instructions.  Over a whole call 4.2 TB/s (48
-// sequences of up to 8192 tokens, 64 / 8 heads of 128: 58.6 us) and 4.7 TB/s
-// (two of 131072: 65.0 us) remain: a CTA takes about 6 us until its first tile
+// HBM; in the loop it takes about 870, that is 5.9 TB/s, also where the cache
+// lies in L2: what bounds it is instructions.  Over a whole call 4.3 TB/s (48
+// sequences of up to 8192 tokens, 64 / 8 heads of 128: 56.7 us) and 4.8 TB/s
+// (two of 131072: 62.7 us) remain: a CTA takes about 6 us until its first tile
 // is there (lengths, page ids and tiles are three trips to memory one after
 // another) and 2 us to join its warps, the cut items 3 to 5 us.
 //
@@ -220,8 +220,11 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   __shared__ int red[kWarps];
   __shared__ RowInfo row_info[R];
 
-  // from lane 0, so that the compiler takes it, and branches on it, as uniform
-  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // warp: from lane 0, so that the compiler takes it, and branches on it, as
+  // uniform.  lane: by a shuffle, or it would be read anew, with all that
+  // follows from it, in every tile (11 instructions).
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+  const int lane = __shfl_sync(0xFFFFFFFFu, threadIdx.x & 31, threadIdx.x & 31);
   const int g = lane >> 2, l4 = lane & 3;
   const nvfp4_kv_cache& c = p.a.c;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
@@ -317,10 +320,14 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       if (k >= mine || tok >= s.lk) return -1;
       return row_table[tok >> p.page_shift];  // (looked at when it is used: a look waits for the load)
     };
-    // lane i: pages of tile i of the 32 that are next
-    int ids0 = page_at(lane, 0), ids1 = page_at(lane, 1);
-    uint32_t bad0 = 0, bad1 = 0;  // bit i: no page there (zeros are written)
-    uint32_t none_next = 0;       // of the tile requested last: bit `half`, no page
+    // Lane i + 16 h keeps half h of tile i of the 16 that are next: its page, and
+    // from its first use on where its rows lie from a head's in page 0 on
+    // (worked out by a lane a half and not by all lanes for each tile: 13
+    // instructions a tile less).
+    int id = page_at(lane & 15, lane >> 4);
+    uint64_t code_off = 0, scale_off = 0;
+    uint32_t bad = 0;        // bit i + 16 h: no page there (zeros are written)
+    uint32_t none_next = 0;  // of the tile requested last: bit h, no page
     int requested = 0;
     // The queries' loads go out before the tiles': behind them they would wait
     // for the whole GPU's first requests to be served.  A thread takes 8
@@ -352,32 +359,26 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     const uint64_t k_src = reinterpret_cast<uint64_t>(c.k_codes + head_codes) + lane * 16;
     const uint64_t v_src = reinterpret_cast<uint64_t>(c.v_codes + head_codes) + lane * 16;
     const uint32_t code_dst = ring_u + lane * 16;
-    // page strides are below 2^32 bytes: one 32 x 32 -> 64 multiply-add
-    const uint32_t code_page = static_cast<uint32_t>(c.code_page_stride);
-    const uint32_t scale_page = static_cast<uint32_t>(c.scale_page_stride);
     int fill = 0;  // ring position of the next request, in bytes
     auto request = [&]() {
       if (requested < mine) {
-        const int at = requested & 31;
-        if (at == 0) {  // the first use of 32 ids
-          if (requested > 0) {
-            ids0 = page_at(requested + lane, 0);
-            ids1 = page_at(requested + lane, 1);
-          }
-          const bool ok0 = ids0 >= 0 && ids0 < c.num_pages, ok1 = ids1 >= 0 && ids1 < c.num_pages;
-          bad0 = __ballot_sync(0xFFFFFFFFu, !ok0);
-          bad1 = __ballot_sync(0xFFFFFFFFu, !ok1);
-          ids0 = ok0 ? ids0 : 0;
-          ids1 = ok1 ? ids1 : 0;
+        const int at = requested & 15;
+        if (at == 0) {
+          if (requested > 0) id = page_at(requested + (lane & 15), lane >> 4);
+          const bool ok = id >= 0 && id < c.num_pages;
+          bad = __ballot_sync(0xFFFFFFFFu, !ok);
+          const uint32_t page = ok ? id : 0;
+          const uint32_t row = ((s.t0 + ts + warp + (requested + (lane & 15)) * kWarps) * kTile + (lane >> 4) * kHalf) &
+                               (c.page_size - 1);
+          // page strides are below 2^32 bytes: one 32 x 32 -> 64 multiply-add
+          code_off = static_cast<uint64_t>(page) * static_cast<uint32_t>(c.code_page_stride) + row * (D / 2);
+          scale_off = static_cast<uint64_t>(page) * static_cast<uint32_t>(c.scale_page_stride) + row * (D / 16);
         }
-        const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, ids0, at), p1 = __shfl_sync(0xFFFFFFFFu, ids1, at);
-        const uint32_t no0 = (bad0 >> at) & 1u, no1 = (bad1 >> at) & 1u;
+        const uint64_t off0 = __shfl_sync(0xFFFFFFFFu, code_off, at), off1 = __shfl_sync(0xFFFFFFFFu, code_off, at + 16);
+        const uint64_t sc_off = __shfl_sync(0xFFFFFFFFu, scale_off, at + 16 * (sc_part & 1));
+        const uint32_t no0 = (bad >> at) & 1u, no1 = (bad >> (at + 16)) & 1u;
         none_next = no0 + 2 * no1;
         const int n0 = 16 - 16 * no0, n1 = 16 - 16 * no1;
-        const uint32_t row0 = ((s.t0 + ts + warp + requested * kWarps) * kTile) & (c.page_size - 1);
-        const uint32_t row1 = (row0 + kHalf) & (c.page_size - 1);
-        const uint64_t off0 = static_cast<uint64_t>(p0) * code_page + row0 * (D / 2);
-        const uint64_t off1 = static_cast<uint64_t>(p1) * code_page + row1 * (D / 2);
         const uint32_t dst = code_dst + fill;
         copy16<0, 0>(dst, k_src + off0, n0);
         copy16<kCodes + kScales, 0>(dst, v_src + off0, n0);
@@ -389,11 +390,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
           copy16<512 + kHalfBytes, 512>(dst, k_src + off1, n1);
           copy16<512 + kHalfBytes + kCodes + kScales, 512>(dst, v_src + off1, n1);
         }
-        if (kScaleLanes == 8 || sc_part < 4) {
-          const bool second = sc_part & 1;
-          const uint64_t off = static_cast<uint64_t>(second ? p1 : p0) * scale_page + (second ? row1 : row0) * (D / 16);
-          copy16<0, 0>(sc_dst + fill, sc_src + off, second ? n1 : n0);
-        }
+        if (kScaleLanes == 8 || sc_part < 4) copy16<0, 0>(sc_dst + fill, sc_src + sc_off, sc_part & 1 ? n1 : n0);
         ++requested;
         fill = kStageBytes - fill;
       }
