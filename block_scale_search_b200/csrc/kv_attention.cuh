@@ -81,8 +81,9 @@ __device__ __forceinline__ float to_f32(uint16_t v, int type) {
 
 // Scaling of a query row whose largest magnitude is mx: the row goes to FP16
 // times `shrink`, a power of two that puts its maximum into [1, 2) (where the
-// reciprocal is a normal number); Inf and NaN stay what they are.  `factor`
-// turns a dot product into a score in base 2.  It is kept above 0 (a negative
+// reciprocal is a normal number).  A row that holds Inf goes all to NaN: its
+// scores could all be -inf, which stands for hidden ones.  `factor` turns a dot
+// product into a score in base 2.  It is kept above 0 (a negative
 // one turns the row's sign), so that it keeps the order of scores and a hidden
 // score's -inf.
 __device__ __forceinline__ void row_scale(float mx, float scale, float& shrink, float& factor) {
@@ -91,6 +92,7 @@ __device__ __forceinline__ void row_scale(float mx, float scale, float& shrink, 
   factor = __uint_as_float(e << 23) * scale;
   if (factor < 0.0f) factor = -factor, shrink = -shrink;
   if (factor < 0x1p-120f) factor = 0x1p-120f;
+  if (mx == INFINITY) shrink = __uint_as_float(0x7FC00000u);
 }
 
 // One sequence: its first query row, new tokens and cached tokens, whatever the

@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       }
       const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * f;
       if (__any_sync(0xFFFFFFFFu, !(mx <= m + kSlack))) {
-        const float top = max3_nan(m, mx, mx);
+        // (inf - inf below would be NaN, which the polynomial does not keep)
+        float top = max3_nan(m, mx, mx);
+        if (top == INFINITY) top = __uint_as_float(0x7FC00000u);
         const float r = top == m ? 1.0f : exp2_approx(m - top);
         m = top;
         down = top == -INFINITY ? 0.0f : -top;

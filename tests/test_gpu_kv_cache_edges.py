@@ -1,0 +1,85 @@
+"""The K/V cache at the ends of its numbers and arguments, on a B200: the default
+stream's handle, queries that hold Inf, rows whose elements lie far apart,
+weights far below a row's largest, NaN in parts of a row that weigh nothing."""
+import pytest
+import torch
+
+from test_gpu_kv_cache import BF16, DEV, FP16, build_batch, check, decode, make_cache, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import block_scale_search_b200 as nv
+    nv.lib()
+    assert torch.cuda.is_available()
+    yield nv
+    assert nv.nvfp4_debug_kv_stalls() == 0
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# --------------------------------------------------------- queries with Inf
+
+def one_sequence(nv, gen, K, V, Q):
+    """A cache that holds rows K, V [tokens, heads, dim], and one sequence's arguments."""
+    n, heads, dim = K.shape
+    S = torch.full((heads,), 2.0 ** -9, device=DEV)
+    pages, table = build_batch(gen, [n], 16)
+    cache = nv.KVCache.empty(pages, 16, heads, dim, S, S)
+    t = torch.arange(n)
+    nv.kv_append(cache, K.to(DEV), V.to(DEV), (table[0, t // 16].long() * 16 + t % 16).to(DEV))
+    return cache, Q.to(DEV), ints(0, Q.shape[0]), ints(n), table.to(DEV), Q.shape[0], n
+
+
+@pytest.mark.parametrize("sign", [1, -1, 0])
+@pytest.mark.parametrize("lq,lk", [(1, 1), (1, 300), (70, 70), (70, 300)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_inf_in_a_query_gives_nan(nv, sign, lq, lk, dim):
+    """K has one sign (or 0) in the query's infinite channel: every score is inf, -inf or NaN, the softmax of none a number."""
+    gen = torch.Generator().manual_seed(lq + lk)
+    K, V = (torch.randn(lk, 2, dim, generator=gen).to(BF16) for _ in range(2))
+    K[..., 5] = sign * (1 + K[..., 5].abs())
+    Q = torch.randn(lq, 4, dim, generator=gen).to(BF16)
+    args = one_sequence(nv, gen, K, V, Q)
+    q = args[1].clone()
+    bad = torch.zeros(lq, 4, dtype=torch.bool, device=DEV)
+    for i, h, x in ((0, 1, float("inf")), (lq - 1, 2, -float("inf")), (lq // 2, 0, float("inf"))):
+        args[1][i, h, 5] = x
+        bad[i, h] = True
+    out, lse = nv.kv_attention(*args, want_lse=True)
+    assert bool(torch.isnan(out[bad]).all()) and bool(torch.isnan(lse[bad]).all())
+    # (the running maxima of a warp's rows move together, so other rows may differ in their rounding:
+    # both results are within the formula's bounds)
+    o, l, to, tl = reference(args[0], q, [lq], [lk], args[4], dim ** -0.5, True, 0)
+    o[bad.cpu()], l[bad.cpu()] = float("nan"), float("nan")
+    check(lse, l, tl, "lse")
+    check(out, o, to, "out")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_inf_scores_in_few_columns_give_nan(nv, dim):
+    """A prompt row whose scores are +inf at tokens 6, 7, 14, 15, .. and -inf at all others."""
+    gen = torch.Generator().manual_seed(3)
+    K, V = (torch.randn(256, 1, dim, generator=gen).to(BF16) for _ in range(2))
+    K[..., 5] = torch.where(torch.arange(256) % 8 >= 6, 2.0, -2.0)[:, None]
+    Q = torch.randn(80, 2, dim, generator=gen).to(BF16)
+    Q[7, 1, 5] = float("inf")
+    args = one_sequence(nv, gen, K, V, Q)
+    out, lse = nv.kv_attention(*args, causal=False, want_lse=True)
+    bad = torch.zeros(80, 2, dtype=torch.bool, device=DEV)
+    bad[7, 1] = True
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(lse), bad)
+    assert bool(torch.isfinite(out[~bad]).all())
+
+
+@pytest.mark.parametrize("lq", [1, 70])
+def test_inf_query_that_sees_nothing(nv, lq):
+    gen = torch.Generator().manual_seed(4)
+    K, V = (torch.randn(20, 2, 64, generator=gen).to(BF16) for _ in range(2))
+    cache, Q, off, _, table, _, _ = one_sequence(nv, gen, K, V, torch.full((lq, 4, 64), float("inf")).to(BF16))
+    out, lse = nv.kv_attention(cache, Q, off, ints(0), table, lq, 20, want_lse=True)
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())
