@@ -728,7 +728,9 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __
   float m = ml.x;
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  // splits that saw no token are left out
+  // splits that saw no token are left out, but none whose weight is 0 in 32
+  // bits: 0 times the NaN of a V that the row sees is NaN
+  const uint32_t saw = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);
   const float z = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
   float l = z * ml.y;
 #pragma unroll
@@ -739,7 +741,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __
   for (int i0 = 0; i0 < p.splits; i0 += 32 / kLanes) {
     const int i = i0 + half;
     const float zi = __shfl_sync(0xFFFFFFFFu, z, i & 31);
-    if (i < p.splits && zi != 0.0f) {
+    if (i < p.splits && (saw >> i) & 1) {
       const float4 v = *reinterpret_cast<const float4*>(p.split_o + at(i) * D + 4 * el);
       acc.x += zi * v.x, acc.y += zi * v.y, acc.z += zi * v.z, acc.w += zi * v.w;
     }

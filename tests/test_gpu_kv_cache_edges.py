@@ -83,3 +83,30 @@ def test_inf_query_that_sees_nothing(nv, lq):
     cache, Q, off, _, table, _, _ = one_sequence(nv, gen, K, V, torch.full((lq, 4, 64), float("inf")).to(BF16))
     out, lse = nv.kv_attention(cache, Q, off, ints(0), table, lq, 20, want_lse=True)
     assert not bool(out.any()) and bool((lse == -float("inf")).all())
+
+
+# ------------------------------------------------------------- NaN in the cache
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lq,heads", [(40, 8), (300, 2), (2, 8)])
+def test_nan_v_of_no_weight_reaches_the_rows_that_see_it(nv, dim, lq, heads):
+    """The NaN token's weight is about 2^-300: 0 in 32 bits, and still 0 NaN = NaN."""
+    gen = torch.Generator().manual_seed(5)
+    n = 6000
+    pages, table = build_batch(gen, [n], 16)
+    cache = make_cache(nv, gen, pages, 16, 1, dim, scale_lo=0x38, scale_hi=0x39)
+    cache.k_S.fill_(1.0)
+    cache.k_codes[..., 0] &= 0xF0
+    t = n - lq - 20                                   # a token that every row sees
+    cache.k_codes[table[0, t // 16], 0, t % 16, 0] = 7
+    Q = torch.randn(lq, heads, dim, generator=gen) * 0.01
+    Q[..., 0] = 4.0
+    Q = Q.to(BF16).to(DEV)
+    args = (cache, Q, ints(0, lq), ints(n), table.to(DEV), lq, n, 300 * 0.6931471805599453 / 24.0)
+    good, good_lse = nv.kv_attention(*args, want_lse=True)
+    assert bool(torch.isfinite(good).all())
+    cache.v_scales[table[0, 100 // 16], 0, 100 % 16, 2] = 0x7F
+    out, lse = nv.kv_attention(*args, want_lse=True)
+    assert bool(torch.isnan(out[..., 32:48]).all())
+    assert torch.equal(out[..., :32], good[..., :32]) and torch.equal(out[..., 48:], good[..., 48:])
+    assert torch.equal(lse, good_lse)
