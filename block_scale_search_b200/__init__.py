@@ -980,7 +980,10 @@ def _on(call, device, stream):
         if stream is None:
             return call(torch._C._cuda_getCurrentRawStream(index))
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+            # (ExternalStream takes 0 for no handle and gives a stream of torch's pool)
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError("stream must be on the cache's device")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 

@@ -110,3 +110,33 @@ def test_nan_v_of_no_weight_reaches_the_rows_that_see_it(nv, dim, lq, heads):
     assert bool(torch.isnan(out[..., 32:48]).all())
     assert torch.equal(out[..., :32], good[..., :32]) and torch.equal(out[..., 48:], good[..., 48:])
     assert torch.equal(lse, good_lse)
+# ------------------------------------------------------------------ streams
+
+def test_stream_0_is_the_default_stream(nv):
+    """What torch.cuda.default_stream().cuda_stream gives: calls follow the work queued there."""
+    assert torch.cuda.default_stream().cuda_stream == 0
+    gen = torch.Generator().manual_seed(1)
+    S = torch.full((2,), 2e-3, device=DEV)
+    slots = torch.arange(32, device=DEV)
+    K, V = (torch.randn(32, 2, 64, generator=gen).to(BF16).to(DEV) for _ in range(2))
+    Q = torch.randn(1, 4, 64, generator=gen).to(BF16).to(DEV)
+    off, lens, table = ints(0, 1), ints(32), ints(0, 1)[None]
+    want = nv.KVCache.empty(3, 16, 2, 64, S, S)
+    nv.kv_append(want, K, V, slots)
+    out_want = nv.kv_attention(want, Q, off, lens, table, 1, 32)
+    read_want = nv.kv_read(want, slots)
+    got = nv.KVCache.empty(3, 16, 2, 64, S, S)
+    x, y, q = torch.zeros_like(K), torch.zeros_like(V), torch.zeros_like(Q)
+    x.copy_(x), torch.cuda._sleep(10), torch.cuda.Stream()   # loaded and set up before it counts
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)          # about 0.1 s: what does not wait for it sees zeros
+    x.copy_(K), y.copy_(V), q.copy_(Q)
+    nv.kv_append(got, x, y, slots, stream=0)
+    nv.kv_copy_pages(got, [0], [2], stream=0)
+    read = nv.kv_read(got, slots, stream=0)
+    out = nv.kv_attention(got, q, off, lens, table, 1, 32, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got.k_codes[:2], want.k_codes[:2]) and torch.equal(got.v_scales[:2], want.v_scales[:2])
+    assert torch.equal(got.k_codes[2], want.k_codes[0])
+    assert all(torch.equal(a, b) for a, b in zip(read, read_want))
+    assert torch.equal(out, out_want)
