@@ -21,8 +21,8 @@
 //     takes the d of its own 16-byte piece of a K row; for O^T lane g owns
 //     head_dim / 8 consecutive d, and the k index runs over tokens.
 //   - a value is code * scale, exact in FP16 (6 bits); S is applied to the
-//     scores and to the result.  Q goes to FP16 after an exact power-of-two
-//     scaling per row, P in (0, 2^8] is rounded to FP16 (2^-11 relative, below
+//     scores and to the result.  Q goes to FP16 after a power-of-two scaling
+//     per row (row_scale: exact but for what lies 2^32 below a row's largest), P in (0, 2^8] is rounded to FP16 (2^-11 relative, below
 //     the rounding of a 16-bit result); sums and the running maximum are FP32.
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
@@ -399,7 +399,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) request();
 
-    // ---- query rows in FP16, a row's maximum scaled to [1, 2), as the lanes
+    // ---- query rows in FP16, scaled, as the lanes
     // of every warp will read them: lane (g, l4) has d [l4 D/4, (l4+1) D/4) of
     // row g of an 8-row tile, word w of it at [tile][w][lane]
 #pragma unroll

@@ -140,3 +140,27 @@ def test_stream_0_is_the_default_stream(nv):
     assert torch.equal(got.k_codes[2], want.k_codes[0])
     assert all(torch.equal(a, b) for a, b in zip(read, read_want))
     assert torch.equal(out, out_want)
+
+
+# ------------------------------------------- query elements that lie far apart
+
+@pytest.mark.parametrize("lq", [1, 70])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kind,top,low", [(FP16, 2.0 ** 15, 2.0 ** -5), (FP16, 60000.0, 2.0 ** -9),
+                                          (BF16, 2.0 ** 20, 2.0 ** -5), (BF16, 3e38, 3e30)])
+def test_small_elements_beside_a_large_one(nv, kind, top, low, dim, lq):
+    """A row's large element meets zeros of K: its small ones alone make the scores."""
+    gen = torch.Generator().manual_seed(lq + dim)
+    kv_len = [150, 333]
+    pages, table = build_batch(gen, kv_len, 16)
+    cache = make_cache(nv, gen, pages, 16, 2, dim)
+    cache.k_codes[..., 0] &= 0xF0
+    Q = (torch.randn(2 * lq, 4, dim, generator=gen) * low).to(kind)
+    Q[..., 0] = top
+    Q = Q.to(DEV)
+    scale = 0.05 / low if low < 1 else 0.05e-30 / 3
+    out, lse = nv.kv_attention(cache, Q, ints(0, lq, 2 * lq), ints(*kv_len), table.to(DEV), lq, max(kv_len), scale,
+                               want_lse=True)
+    o, l, to, tl = reference(cache, Q, [lq, lq], kv_len, table, scale, True, 0)
+    check(lse, l, tl, "lse")
+    check(out, o, to, "out")
