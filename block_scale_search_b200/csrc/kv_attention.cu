@@ -22,8 +22,9 @@
 //     head_dim / 8 consecutive d, and the k index runs over tokens.
 //   - a value is code * scale, exact in FP16 (6 bits); S is applied to the
 //     scores and to the result.  Q goes to FP16 after a power-of-two scaling
-//     per row (row_scale: exact but for what lies 2^32 below a row's largest), P in (0, 2^8] is rounded to FP16 (2^-11 relative, below
-//     the rounding of a 16-bit result); sums and the running maximum are FP32.
+//     per row (exact but for what lies 2^32 below a row's largest), and so does
+//     P, scaled so that the largest is 2^7 to 2^15 (2^-11 relative, below the
+//     rounding of a 16-bit result); sums and the running maximum are FP32.
 //   - the running maximum moves only when a score passes it by 2^8 (P stays
 //     in FP16 range until then): one vote per tile in place of a reduction.
 // A tile of 32 tokens takes 640 instructions at head_dim 128 with 8 rows, 140
@@ -446,11 +447,14 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     const int all_hi = __shfl_sync(0xFFFFFFFFu, row_info[0].hi, 0);
 
     float o[NT][VW * 4][4] = {};
-    // running maximum (base-2 exponent), what to add to a score for it (0 while
-    // nothing was seen), and this lane's share of the sum
-    float m[NT][2], down[NT][2] = {}, l[NT][2] = {};
+    // what is added to a score (-m; 0 while nothing was seen), the value that the
+    // sum may not pass (-inf until then, so that the first score passes it), and
+    // this lane's share of the sum of P.  (Compared is what the exponentials
+    // get, the same fma: a score and m round apart where they are large.)
+    float down[NT][2] = {}, limit[NT][2], l[NT][2] = {};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY;
+    for (int n = 0; n < NT; ++n) limit[n][0] = limit[n][1] = -INFINITY;
+    auto at_m = [&](int n, int i) { return limit[n][i] == -INFINITY ? -INFINITY : -down[n][i]; };
 
     // S^T row r holds token r ^ (r >> 1 & 1): neighbouring rows and the
     // tokens of one V load then differ in parity, which halves the bank
@@ -526,8 +530,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          over |= fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])) * f[n][i] >
-                  m[n][i] + kSlack;
+          over |= fmaf(fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])), f[n][i],
+                       down[n][i]) > limit[n][i];
       }
       if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -538,10 +542,10 @@ kv_rows_kernel(const __grid_constant__ Params p) {
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-            t = fmaxf(t, m[n][i]);
-            const float r = t == m[n][i] ? 1.0f : exp2_approx(m[n][i] - t);
-            m[n][i] = t;
-            down[n][i] = t == -INFINITY ? 0.0f : -t;
+            const float m = at_m(n, i);
+            t = fmaxf(t - kAim, m);
+            const float r = t == m ? 1.0f : exp2_approx(m - t);
+            if (t != -INFINITY) down[n][i] = -t, limit[n][i] = kTop;
             l[n][i] *= r;
 #pragma unroll
             for (int u = 0; u < VW * 4; ++u) o[n][u][i] *= r, o[n][u][i + 2] *= r;
@@ -651,7 +655,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         t += __shfl_xor_sync(0xFFFFFFFFu, t, 16);
         const int col = 8 * n + 2 * l4 + i;
         if (g == 0) {
-          join_ml[(warp * R + col) * 2] = m[n][i];
+          join_ml[(warp * R + col) * 2] = at_m(n, i);
           join_ml[(warp * R + col) * 2 + 1] = t;
         }
         float* dst = join_o + (warp * R + col) * D + g * (D / 8);

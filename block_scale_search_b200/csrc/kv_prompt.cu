@@ -353,7 +353,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : 0;
     };
     int page = 0;
-    float m = -INFINITY, down = 0.0f, l = 0.0f;
+    // what is added to a score (-m; 0 while nothing was seen), what the sum may
+    // not pass, and the sum of P, as in kv_rows_kernel
+    float down = 0.0f, limit = -INFINITY, l = 0.0f;
+    auto at_m = [&] { return limit == -INFINITY ? -INFINITY : -down; };
     const int from = t ? tile_from[1] : tile_from[0], to = t ? tile_to[1] : tile_to[0];
     page = page_of(from);
     for (int i = from; i < to; ++i) {
@@ -396,14 +399,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         }
         m4[q] = max3_nan(a, z, z);
       }
-      const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * f;
-      if (__any_sync(0xFFFFFFFFu, !(mx <= m + kSlack))) {
+      const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+      if (__any_sync(0xFFFFFFFFu, !(fmaf(mx, f, down) <= limit))) {
         // (inf - inf below would be NaN, which the polynomial does not keep)
-        float top = max3_nan(m, mx, mx);
+        const float m = at_m(), next = mx * f - kAim;
+        float top = max3_nan(m, next, next);
         if (top == INFINITY) top = __uint_as_float(0x7FC00000u);
         const float r = top == m ? 1.0f : exp2_approx(m - top);
-        m = top;
-        down = top == -INFINITY ? 0.0f : -top;
+        if (top != -INFINITY) down = -top, limit = kTop;
         l *= r;
         if (i > from) {
 #pragma unroll 1
@@ -469,6 +472,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int i = 0; i < D / 16; ++i) nan_blocks |= (sc[i] & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
       }
     }
+    const float m = at_m();
     if (m == -INFINITY) l = 0.0f;  // saw no token (the sum may hold some 2^-126)
     const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
     const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + t) * kTileRows + (threadIdx.x & 127);

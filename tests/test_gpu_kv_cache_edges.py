@@ -164,3 +164,48 @@ def test_small_elements_beside_a_large_one(nv, kind, top, low, dim, lq):
     o, l, to, tl = reference(cache, Q, [lq, lq], kv_len, table, scale, True, 0)
     check(lse, l, tl, "lse")
     check(out, o, to, "out")
+
+
+# -------------------------------------------------- weights far below the largest
+
+@pytest.mark.parametrize("lq", [1, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bits", [10.0, 16.0, 20.0, 24.4, 25.5, 27.0])
+def test_weights_far_below_the_largest(nv, lq, dim, bits):
+    """Every 32nd token's score is `bits` powers of two above the others' (spread: a third of
+    one), and its V is 0, so that the others are the whole output.
+
+    Bound, per element: P is rounded to FP16 (2^-11 of it; where it is subnormal there, half a
+    step of 2^-24 in units in which the largest P is 2^7 or more: 2^-32 of the largest weight, 1
+    here, so n 2^-32 max|v| / L), scores and exponentials as in reference(), twice."""
+    gen = torch.Generator().manual_seed(int(bits * 10) + lq)
+    n, heads, kvh = 4096, 4, 1
+    pages, table = build_batch(gen, [n], 16)
+    cache = make_cache(nv, gen, pages, 16, kvh, dim, scale_lo=0x38, scale_hi=0x39)
+    cache.k_S.fill_(1.0)
+    sink = torch.arange(0, n, 32)
+    p, r = table[0, sink // 16].long().to(DEV), (sink % 16).to(DEV)
+    cache.k_codes[..., 0] &= 0xF0                     # element 0: 0
+    cache.k_codes[p, 0, r] = 0
+    cache.k_codes[p, 0, r, 0] = 7                     # the sinks': 6, and nothing else
+    cache.v_codes[p, 0, r] = 0
+    Q = torch.randn(lq, heads, dim, generator=gen) * 0.01
+    Q[..., 0] = 4.0
+    Q = Q.to(BF16).to(DEV)
+    scale = bits * 0.6931471805599453 / 24.0
+    out, lse = nv.kv_attention(cache, Q, ints(0, lq), ints(n), table.to(DEV), lq, n, scale, causal=False, want_lse=True)
+    t = torch.arange(n)
+    ids = table[0, t // 16].long()
+    k = decode(cache.k_codes.cpu()[ids, 0, t % 16], cache.k_scales.cpu()[ids, 0, t % 16], cache.k_S[0])
+    v = decode(cache.v_codes.cpu()[ids, 0, t % 16], cache.v_scales.cpu()[ids, 0, t % 16], cache.v_S[0])
+    q = Q.cpu().double()
+    x = q @ k.T * scale
+    X = (q.abs() @ k.abs().T * scale).amax(-1, keepdim=True)
+    m = x.amax(-1, keepdim=True)
+    w = torch.exp(x - m)
+    L = w.sum(-1, keepdim=True)
+    d = 2 ** -18 * X + 2 ** -17
+    o = w @ v / L
+    tol = (w @ v.abs() / L * (2 ** -11 + 2 * d) + n * 2 ** -32 * v.abs().max() / L + o.abs() * 2 ** -8)
+    check(out, o, tol, "out")
+    check(lse, (m + torch.log(L))[..., 0], (d + (m.abs() + torch.log(L)) * 2 ** -21)[..., 0], "lse")
