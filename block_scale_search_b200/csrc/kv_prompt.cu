@@ -690,9 +690,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
             if (now) pv(t, st, kTokens / 32, kTokens / 16, true);
             if (now && !next) tc_commit(bar(kOFull + t));
             if (next) qk(t, nst);
-            if (t == 1) {
+            // (not behind the last step: no one waits for those, and an arrival
+            // could then come after the CTA's end)
+            if (t == 1 && more) {
               tc_commit(bar(kVEmpty + st));
-              if (more) tc_commit(bar(kKEmpty + nst));
+              tc_commit(bar(kKEmpty + nst));
             }
           }
           __syncwarp();
