@@ -40,6 +40,7 @@ __all__ = [
     "diag_hessian", "global_scale", "scale_sweep_quantize", "dequantize", "quantize_layer",
     "KVCacheDesc", "KVCache", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_copy_pages",
     "nvfp4_kv_attention_workspace_size", "nvfp4_kv_attention", "nvfp4_debug_kv_stalls",
+    "nvfp4_debug_kv_wait_limit",
     "kv_append", "kv_read", "kv_copy_pages", "kv_attention",
 ]
 
@@ -169,6 +170,7 @@ _SIGS = {
                             _i64, _i64, _i64, _i64, _f32, _int, _i64, _vp, _i64, _i64, _vp, _vp, _sz,
                             _vp], _int),
     "nvfp4_debug_kv_stalls": ([C.POINTER(C.c_uint), _int], _int),
+    "nvfp4_debug_kv_wait_limit": ([_i64], _int),
     "nvfp4_scale_sweep_quantize_batched_workspace_size": ([_i64], _sz),
     "nvfp4_scale_sweep_quantize_batched": ([C.POINTER(SweepDesc), _i64, _int, _int, _vp, _sz, _vp],
                                            _int),
@@ -537,6 +539,11 @@ def nvfp4_debug_kv_stalls(reset: bool = False) -> int:
     n = C.c_uint(0)
     _check("nvfp4_debug_kv_stalls", lib().nvfp4_debug_kv_stalls(C.byref(n), int(bool(reset))))
     return n.value
+
+
+def nvfp4_debug_kv_wait_limit(cycles: int) -> None:
+    """Cycles after which such a wait is given up; the bounds-checked build only."""
+    _check("nvfp4_debug_kv_wait_limit", lib().nvfp4_debug_kv_wait_limit(cycles))
 
 
 # -------------------------------------------------------- tensor conveniences

@@ -13,6 +13,7 @@
 namespace nvfp4 {
 int record_cuda_status(cudaError_t e);
 unsigned int kv_stalls(bool reset, cudaError_t* e);
+bool kv_wait_limit(long long cycles, cudaError_t* e);
 }  // namespace nvfp4
 
 namespace {
@@ -231,6 +232,12 @@ int nvfp4_debug_kv_stalls(unsigned int* count, int reset) {
   if (count == nullptr || (reset != 0 && reset != 1)) return NVFP4_ERR_INVALID_ARG;
   cudaError_t e = cudaSuccess;
   *count = nvfp4::kv_stalls(reset != 0, &e);
+  return nvfp4::record_cuda_status(e);
+}
+
+int nvfp4_debug_kv_wait_limit(int64_t cycles) {
+  cudaError_t e = cudaSuccess;
+  if (cycles < 0 || !nvfp4::kv_wait_limit(cycles, &e)) return NVFP4_ERR_INVALID_ARG;
   return nvfp4::record_cuda_status(e);
 }
 

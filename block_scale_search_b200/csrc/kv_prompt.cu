@@ -45,6 +45,18 @@ constexpr int kPromptThreads = 32 * kPromptWarps;
 constexpr int kHalfTile = kTokens * 128;    // bytes: 128 rows of 64 elements
 
 __device__ unsigned int g_stalls;           // waits given up
+// Cycles after which a wait is given up, every how many tries (a power of two)
+// it looks at the clock, and the instruction that tries: try_wait may hold the
+// warp a while.  Tests of the checked build set the limit, to 0 too.
+#ifdef NVFP4HS_CHECKS
+__device__ long long g_wait_limit = 1ll << 32;
+constexpr uint32_t kLookEvery = 1;
+#define NVFP4_MBAR_TRY "mbarrier.test_wait"
+#else
+constexpr long long g_wait_limit = 1ll << 32;
+constexpr uint32_t kLookEvery = 256;
+#define NVFP4_MBAR_TRY "mbarrier.try_wait"
+#endif
 
 // Shared memory from a 1024-byte boundary: Q of both tiles, two stages of K,
 // two of V, and three slots of packed rows (K or V of a step).
@@ -83,24 +95,25 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      "{ .reg .pred p; " NVFP4_MBAR_TRY ".parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
 // Waits for a phase, for about two seconds at most: a wait given up is counted
-// and ends all later ones of the CTA, which then runs to its end.
+// and ends all later ones of the CTA, which then runs to its end and leaves NaN.
 template <int kSleep>
 __device__ __forceinline__ void mbar_wait_slow(Shared* sh, uint32_t bar, uint32_t parity) {
   long long t0 = 0;
   for (uint32_t n = 1;; ++n) {
     if constexpr (kSleep > 0) __nanosleep(kSleep);
     if (mbar_try(bar, parity)) return;
-    if ((n & 255u) != 0) continue;
+    if ((n & (kLookEvery - 1)) != 0) continue;
     if (*reinterpret_cast<volatile int*>(&sh->gave_up)) return;
     if (t0 == 0) t0 = clock64();
-    if (clock64() - t0 > (1ll << 32)) {
+    if (clock64() - t0 > g_wait_limit) {
       atomicAdd(&g_stalls, 1u);
       *reinterpret_cast<volatile int*>(&sh->gave_up) = 1;
+      __threadfence_block();  // before what this warp makes of the unfinished phase
       return;
     }
   }
@@ -472,7 +485,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         for (int i = 0; i < D / 16; ++i) nan_blocks |= (sc[i] & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
       }
     }
-    const float m = at_m();
+    float m = at_m();
+    // No number of an unfinished phase leaves the CTA as a result.
+    if (*reinterpret_cast<volatile int*>(&sh.gave_up)) m = l = __uint_as_float(0x7FC00000u);
     if (m == -INFINITY) l = 0.0f;  // saw no token (the sum may hold some 2^-126)
     const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
     const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + t) * kTileRows + (threadIdx.x & 127);
@@ -813,6 +828,18 @@ cudaError_t launch_kv_prompt(Params& p, const PromptPlan& plan, void* workspace,
   p.split_o = static_cast<float*>(workspace);
   p.split_ml = reinterpret_cast<float2*>(p.split_o + plan.items * plan.splits * kRows * p.a.c.head_dim);
   return p.a.c.head_dim == 128 ? run_prompt<128>(p, stream) : run_prompt<64>(p, stream);
+}
+
+// False where the limit is built in.
+bool kv_wait_limit(long long cycles, cudaError_t* e) {
+#ifdef NVFP4HS_CHECKS
+  *e = cudaMemcpyToSymbol(g_wait_limit, &cycles, sizeof(cycles));
+  return true;
+#else
+  (void)cycles;
+  *e = cudaSuccess;
+  return false;
+#endif
 }
 
 unsigned int kv_stalls(bool reset, cudaError_t* e) {

@@ -716,8 +716,12 @@ int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* Q, int type, int
                        size_t workspace_bytes, void* stream);
 
 /* Test support: how often a wait inside the attention kernels was given up
- * (they are bounded; never in a correct run).  Synchronises with the device. */
+ * (they end after 2^32 cycles; never in a correct run).  The rows whose waits
+ * were given up are NaN in out and lse.  Synchronises with the device. */
 int nvfp4_debug_kv_stalls(unsigned int* count, int reset);
+/* Test support: the cycles after which such a wait is given up, in the
+ * bounds-checked build; NVFP4_ERR_INVALID_ARG in the normal one. */
+int nvfp4_debug_kv_wait_limit(int64_t cycles);
 
 #ifdef __cplusplus
 }
