@@ -1049,12 +1049,27 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
     return _on(call, cache.device, stream)
 
 
+def _page_ids(t, name):
+    """t as a contiguous int32 CPU tensor; whole numbers that fit alone."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cpu and t.is_contiguous():
+        return t
+    try:
+        t = torch.as_tensor(t, device="cpu")
+    except (TypeError, ValueError, RuntimeError, OverflowError) as e:
+        raise ValueError(f"{name} must be a list of page ids") from e
+    if t.numel() == 0:
+        return t.int()
+    n = t.to(torch.int32)
+    if t.dtype is torch.bool or t.is_floating_point() or t.is_complex() or not torch.equal(n.to(t.dtype), t):
+        raise ValueError(f"{name} must be page ids, whole numbers of 32 bits")
+    return n.contiguous()
+
+
 def kv_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     """Page dst[i] becomes page src[i] in every layer of the cache.  src, dst: page
-    ids on the host (int32 CPU tensors or sequences); no page may be written
-    twice, or both read and written."""
-    src, dst = (t if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cpu and t.is_contiguous()
-                else torch.as_tensor(t, dtype=torch.int32, device="cpu").contiguous() for t in (src, dst))
+    ids on the host (int32 CPU tensors, or whole numbers of another kind that
+    fit); no page may be written twice, or both read and written."""
+    src, dst = _page_ids(src, "src"), _page_ids(dst, "dst")
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be lists of as many pages")
     many = cache.k_codes.dim() == 5
