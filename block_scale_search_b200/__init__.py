@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 import os
 import threading
 
@@ -888,22 +889,27 @@ class KVCache:
     v_scales uint8 [pages, kv_heads, page_size, head_dim/16] and k_S, v_S float32
     [kv_heads], all CUDA.  Each may have a leading dimension of layers; a cache of
     several layers serves kv_copy_pages, and layer(i) is one of its layers.
-    Pages (and layers) may have any stride; a page is contiguous."""
+    Pages (and layers) may have any stride; a page is contiguous.  A cache keeps
+    the addresses of its tensors: they may be written, but not replaced (make
+    another KVCache of the new ones)."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_S", "v_S", "layers", "device", "desc")
+    __slots__ = ("_k_codes", "_k_scales", "_v_codes", "_v_scales", "_k_S", "_v_S", "_layers", "_device", "_desc")
+    # (read only: a tensor put in the place of another would not be the one used)
+    k_codes, k_scales, v_codes, v_scales, k_S, v_S, layers, device, desc = (
+        property(operator.attrgetter(name)) for name in __slots__)
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_S, v_S):
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_S, self.v_S = k_S, v_S
+        self._k_codes, self._k_scales, self._v_codes, self._v_scales = k_codes, k_scales, v_codes, v_scales
+        self._k_S, self._v_S = k_S, v_S
         shape, stride = k_codes.shape, k_codes.stride()
         if len(shape) == 4:
             pages, h, p, half = shape
             page_stride, s1, s2, s3 = stride
-            lead, s_shape, self.layers = (), (h,), 1
+            lead, s_shape, self._layers = (), (h,), 1
         elif len(shape) == 5:
             layers, pages, h, p, half = shape
             _, page_stride, s1, s2, s3 = stride
-            lead, s_shape, self.layers = (layers,), (layers, h), layers
+            lead, s_shape, self._layers = (layers,), (layers, h), layers
         else:
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim/2], or that after layers")
         dim, groups = 2 * half, half // 8
@@ -915,7 +921,7 @@ class KVCache:
             raise ValueError("K and V must have the same strides")
         if s3 != 1 or s2 != half or s1 != p * half or small_stride[-3:] != (p * groups, groups, 1):
             raise ValueError("a page must be contiguous")
-        self.device = k_codes.device
+        self._device = k_codes.device
         where = k_codes.get_device()  # -1 on the CPU
         u8, f32 = torch.uint8, torch.float32
         if (where < 0 or k_codes.dtype is not u8 or k_scales.dtype is not u8 or v_codes.dtype is not u8
@@ -925,9 +931,9 @@ class KVCache:
             raise ValueError("codes and scales must be uint8, S float32, on one CUDA device")
         if k_S.shape != s_shape or v_S.shape != s_shape or not k_S.is_contiguous() or not v_S.is_contiguous():
             raise ValueError("S must be contiguous [kv_heads], or [layers, kv_heads]")
-        self.desc = KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), pages,
-                                page_stride, small_stride[-4], p, h, dim)
+        self._desc = KVCacheDesc(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                 v_scales.data_ptr(), k_S.data_ptr(), v_S.data_ptr(), pages,
+                                 page_stride, small_stride[-4], p, h, dim)
 
     @classmethod
     def empty(cls, pages, page_size, kv_heads, head_dim, k_S, v_S, layers=None):
@@ -956,9 +962,9 @@ class KVCache:
 
 
 def _one_layer(cache):
-    if cache.k_codes.dim() != 4:
+    if cache._k_codes.dim() != 4:
         raise ValueError("pass one layer of the cache (cache.layer(i))")
-    return cache.desc
+    return cache._desc
 
 
 def _kv_rows(t, name, heads, dim, device, types):
@@ -1008,32 +1014,32 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
     slots (int64 [tokens], page * page_size + row; negative: skipped; the others
     distinct).  status: int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN."""
     d = _one_layer(cache)
-    _kv_rows(K, "K", d.kv_heads, d.head_dim, cache.device, _TYPES)
-    _kv_rows(V, "V", d.kv_heads, d.head_dim, cache.device, (K.dtype,))
+    _kv_rows(K, "K", d.kv_heads, d.head_dim, cache._device, _TYPES)
+    _kv_rows(V, "V", d.kv_heads, d.head_dim, cache._device, (K.dtype,))
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError("K and V must have as many tokens")
-    _int_vector(slots, "slots", torch.int64, cache.device, n)
+    _int_vector(slots, "slots", torch.int64, cache._device, n)
     if status is not None:
-        _int_vector(status, "status", torch.int32, cache.device, 1)
+        _int_vector(status, "status", torch.int32, cache._device, 1)
     k0, k1, _ = K.stride()
     v0, v1, _ = V.stride()
     kind = _TYPES[K.dtype]
     _on(lambda handle: _check("nvfp4_kv_append", lib().nvfp4_kv_append(
         C.byref(d), K.data_ptr(), V.data_ptr(), kind, n, k0, k1, v0, v1, slots.data_ptr(), _ptr(status), handle)),
-        cache.device, stream)
+        cache._device, stream)
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, out=None, stream=None):
     """The rows at slots as numbers: (K, V) [tokens, kv_heads, head_dim] of dtype; 0
     where a slot is negative.  out: a pair of contiguous tensors to write."""
     d = _one_layer(cache)
-    _int_vector(slots, "slots", torch.int64, cache.device)
+    _int_vector(slots, "slots", torch.int64, cache._device)
     if dtype not in _TYPES:
         raise ValueError("dtype must be bfloat16, float16 or float32")
     n = slots.numel()
     if out is not None:
-        K, V = (_kv_rows(t, "out", d.kv_heads, d.head_dim, cache.device, (dtype,)) for t in out)
+        K, V = (_kv_rows(t, "out", d.kv_heads, d.head_dim, cache._device, (dtype,)) for t in out)
         if not (K.is_contiguous() and V.is_contiguous() and K.shape[0] == V.shape[0] == n):
             raise ValueError("out must be two contiguous tensors with a row for every slot")
 
@@ -1041,12 +1047,12 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
         if out is not None:
             k, v = out
         else:
-            k, v = torch.empty(2, n, d.kv_heads, d.head_dim, dtype=dtype, device=cache.device).unbind(0)
+            k, v = torch.empty(2, n, d.kv_heads, d.head_dim, dtype=dtype, device=cache._device).unbind(0)
         _check("nvfp4_kv_read", lib().nvfp4_kv_read(C.byref(d), slots.data_ptr(), n, _TYPES[dtype], k.data_ptr(),
                                                     v.data_ptr(), handle))
         return k, v
 
-    return _on(call, cache.device, stream)
+    return _on(call, cache._device, stream)
 
 
 def _page_ids(t, name):
@@ -1072,10 +1078,10 @@ def kv_copy_pages(cache: KVCache, src, dst, stream=None) -> None:
     src, dst = _page_ids(src, "src"), _page_ids(dst, "dst")
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be lists of as many pages")
-    many = cache.k_codes.dim() == 5
-    _on(lambda handle: nvfp4_kv_copy_pages(cache.desc, cache.layers, cache.k_codes.stride(0) if many else 0,
-                                           cache.k_scales.stride(0) if many else 0, src, dst, src.numel(), handle),
-        cache.device, stream)
+    many = cache._k_codes.dim() == 5
+    _on(lambda handle: nvfp4_kv_copy_pages(cache._desc, cache._layers, cache._k_codes.stride(0) if many else 0,
+                                           cache._k_scales.stride(0) if many else 0, src, dst, src.numel(), handle),
+        cache._device, stream)
 
 
 def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_lengths: torch.Tensor,
@@ -1089,7 +1095,7 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
     of the lengths, known to the host.  sm_scale: 1 / sqrt(head_dim) by default.
     Returns out, or (out, lse) with lse float32 [total, q_heads]."""
     d = _one_layer(cache)
-    dev = cache.device
+    dev = cache._device
     if Q.dim() != 3:
         raise ValueError("Q must be [total, q_heads, head_dim]")
     total, heads, _ = Q.shape
