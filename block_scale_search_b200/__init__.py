@@ -976,6 +976,12 @@ def _kv_rows(t, name, heads, dim, device, types):
     return t
 
 
+def _no_graph(name, requires_grad):
+    if requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and the cache's calls have none: call them under torch.no_grad(), "
+                         "or detach it")
+
+
 def _int_vector(t, name, kind, device, n=None):
     if t.dtype is not kind or t.dim() != 1 or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{name} must be a contiguous {kind} vector" + (f" of {n}" if n is not None else "") +
@@ -1012,10 +1018,12 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
     """Quantizes rows K, V [tokens, kv_heads, head_dim] (bf16, fp16 or float32; any
     token and head strides that are multiples of 16 bytes) into the cache at
     slots (int64 [tokens], page * page_size + row; negative: skipped; the others
-    distinct).  status: int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN."""
+    distinct).  status: int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN.
+    No gradient: K and V that require one are refused (but under torch.no_grad())."""
     d = _one_layer(cache)
     _kv_rows(K, "K", d.kv_heads, d.head_dim, cache._device, _TYPES)
     _kv_rows(V, "V", d.kv_heads, d.head_dim, cache._device, (K.dtype,))
+    _no_graph("K or V", K.requires_grad or V.requires_grad)
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError("K and V must have as many tokens")
@@ -1093,7 +1101,10 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
     tokens, the new ones included.  q_offsets int32 [batch+1], kv_lengths int32
     [batch], page_table int32 [batch, pages per sequence]; max_q, max_kv: bounds
     of the lengths, known to the host.  sm_scale: 1 / sqrt(head_dim) by default.
-    Returns out, or (out, lse) with lse float32 [total, q_heads]."""
+    Returns out, or (out, lse) with lse float32 [total, q_heads].  Rows of no
+    sequence, and a sequence's rows past max_q, are not written: they are left as
+    they were in a given out and lse, and hold anything in new ones.
+    No gradient: a Q that requires one is refused (but under torch.no_grad())."""
     d = _one_layer(cache)
     dev = cache._device
     if Q.dim() != 3:
@@ -1101,6 +1112,7 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, q_offsets: torch.Tensor, kv_le
     total, heads, _ = Q.shape
     dim = d.head_dim
     _kv_rows(Q, "Q", heads, dim, dev, (torch.bfloat16, torch.float16))
+    _no_graph("Q", Q.requires_grad)
     _int_vector(kv_lengths, "kv_lengths", torch.int32, dev)
     batch = kv_lengths.shape[0]
     _int_vector(q_offsets, "q_offsets", torch.int32, dev, batch + 1)
