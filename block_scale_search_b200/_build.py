@@ -11,7 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4hs.so")
 # the checked build: bounds checks on every global access of the per-step
-# kernels (-DNVFP4HS_CHECKS), for debugging and for the edge-case tests
+# kernels and the K/V cache's (-DNVFP4HS_CHECKS), for debugging and for the
+# edge-case tests
 LIB_CHECKED = os.path.join(PKG, "libnvfp4hs_checked.so")
 
 NVCC_FLAGS = [

@@ -200,6 +200,22 @@ __device__ __forceinline__ int2 units_before(const Params& p, int n, int* red) {
 // Units per CTA: an equal share, but no less than a tile a warp.
 __device__ __forceinline__ int units_per_cta(int total, int ctas) { return max((total + ctas - 1) / ctas, kWarps); }
 
+// Where a CTA lists its cut item, and a row's partial sums from element d on,
+// and maximum and sum (R rows an item, two items a CTA).
+__device__ __forceinline__ int4* cut_at(const Params& p, unsigned int cta) {
+  return checked(p.cut + cta, p.cut, static_cast<int64_t>(p.ctas) * 16, kSiteKvCut);
+}
+template <int D, int R>
+__device__ __forceinline__ float4* partial_at(const Params& p, int64_t row, int d) {
+  return checked(reinterpret_cast<float4*>(p.partial + row * D + d), p.partial, static_cast<int64_t>(p.ctas) * 2 * R * D * 4,
+                 kSiteKvPartial);
+}
+template <int R>
+__device__ __forceinline__ float2* partial_ml_at(const Params& p, int64_t row) {
+  return checked(reinterpret_cast<float2*>(p.partial_ml + row * 2), p.partial_ml, static_cast<int64_t>(p.ctas) * 2 * R * 8,
+                 kSiteKvPartial);
+}
+
 // Of a query row of the item: factor of its scores (base 2), visible tokens.
 struct RowInfo {
   float f;
@@ -242,7 +258,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
   int b = 0;
   int base = 0, cur, end;  // base: first unit of sequence b
   __shared__ int share;  // units per CTA, for the list of cut items
-  if (p.cut != nullptr && threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (p.cut != nullptr && threadIdx.x == 0) *cut_at(p, blockIdx.x) = make_int4(0, 0, 0, 0);
   if (p.a.batch <= kThreads) {   // a sequence a thread: one look at the lengths
     const int n = threadIdx.x < p.a.batch ? seq_units<R>(p, threadIdx.x) : 0;
     int inc = warp_scan(n, lane);
@@ -319,7 +335,7 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     auto page_at = [&](int k, int half) {  // the table's entry for half a tile, or -1
       const int tok = (s.t0 + ts + warp + k * kWarps) * kTile + half * kHalf;
       if (k >= mine || tok >= s.lk) return -1;
-      return row_table[tok >> p.page_shift];  // (looked at when it is used: a look waits for the load)
+      return table_entry(p, row_table, tok >> p.page_shift);  // (looked at when it is used: a look waits for the load)
     };
     // Lane i + 16 h keeps half h of tile i of the 16 that are next: its page, and
     // from its first use on where its rows lie from a head's in page 0 on
@@ -343,11 +359,11 @@ kv_rows_kernel(const __grid_constant__ Params p) {
       qv[n] = make_uint4(0u, 0u, 0u, 0u);
       if (qr + n * kPass < R && row < s.lq * p.group) {
         const int qi = row / p.group, gi = row - qi * p.group;
-        qv[n] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.Q) + (s.q0 + qi) * p.a.q_token_stride +
-                                                (h * p.group + gi) * p.a.q_head_stride + 8 * qp);
+        qv[n] = query_piece(p, static_cast<const uint16_t*>(p.a.Q) + (s.q0 + qi) * p.a.q_token_stride +
+                                   (h * p.group + gi) * p.a.q_head_stride + 8 * qp);
       }
     }
-    const float kS = c.k_S[h];
+    const float kS = head_S(p, c.k_S, h);
 
     // scale bytes: lanes 8 i .. 8 i + 7 (D = 64: 4 i .. 4 i + 3) copy those of
     // K (i < 2) or V of half i % 2
@@ -381,17 +397,28 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         none_next = no0 + 2 * no1;
         const int n0 = 16 - 16 * no0, n1 = 16 - 16 * no1;
         const uint32_t dst = code_dst + fill;
-        copy16<0, 0>(dst, k_src + off0, n0);
-        copy16<kCodes + kScales, 0>(dst, v_src + off0, n0);
-        copy16<kHalfBytes, 0>(dst, k_src + off1, n1);
-        copy16<kHalfBytes + kCodes + kScales, 0>(dst, v_src + off1, n1);
+        auto k_at = [&](auto skip, uint64_t off) {
+          return checked_at<uint4, decltype(skip)::value>(k_src + off, c.k_codes, codes_extent(c), kSiteKvCodes);
+        };
+        auto v_at = [&](auto skip, uint64_t off) {
+          return checked_at<uint4, decltype(skip)::value>(v_src + off, c.v_codes, codes_extent(c), kSiteKvCodes);
+        };
+        constexpr std::integral_constant<int, 0> first{};
+        copy16<0, 0>(dst, k_at(first, off0), n0);
+        copy16<kCodes + kScales, 0>(dst, v_at(first, off0), n0);
+        copy16<kHalfBytes, 0>(dst, k_at(first, off1), n1);
+        copy16<kHalfBytes + kCodes + kScales, 0>(dst, v_at(first, off1), n1);
         if constexpr (kCodes == 1024) {
-          copy16<512, 512>(dst, k_src + off0, n0);
-          copy16<512 + kCodes + kScales, 512>(dst, v_src + off0, n0);
-          copy16<512 + kHalfBytes, 512>(dst, k_src + off1, n1);
-          copy16<512 + kHalfBytes + kCodes + kScales, 512>(dst, v_src + off1, n1);
+          constexpr std::integral_constant<int, 512> second{};
+          copy16<512, 512>(dst, k_at(second, off0), n0);
+          copy16<512 + kCodes + kScales, 512>(dst, v_at(second, off0), n0);
+          copy16<512 + kHalfBytes, 512>(dst, k_at(second, off1), n1);
+          copy16<512 + kHalfBytes + kCodes + kScales, 512>(dst, v_at(second, off1), n1);
         }
-        if (kScaleLanes == 8 || sc_part < 4) copy16<0, 0>(sc_dst + fill, sc_src + sc_off, sc_part & 1 ? n1 : n0);
+        if (kScaleLanes == 8 || sc_part < 4) copy16<0, 0>(sc_dst + fill,
+                                                            checked_at<uint4>(sc_src + sc_off, sc_part & 2 ? c.v_scales : c.k_scales,
+                                                                              scales_extent(c), kSiteKvScales),
+                                                            sc_part & 1 ? n1 : n0);
         ++requested;
         fill = kStageBytes - fill;
       }
@@ -671,9 +698,9 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     if (p.cut != nullptr && ts == 0 && !whole && threadIdx.x == 0) {
       // at most one item is cut behind its first tile in this CTA
       // its last tile is tiles - te - 1 units behind this CTA's end
-      p.cut[blockIdx.x] = make_int4(b, item, blockIdx.x, (s.tiles - te - 1) / share + 2);
+      *cut_at(p, blockIdx.x) = make_int4(b, item, blockIdx.x, (s.tiles - te - 1) / share + 2);
     }
-    const float vS = c.v_S[h];
+    const float vS = head_S(p, c.v_S, h);
     const int rows = min(R, s.lq * p.group - r0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
@@ -695,8 +722,8 @@ kv_rows_kernel(const __grid_constant__ Params p) {
         if (d == 0) write_lse(p, s, h, r0 + row, mm, ll);
       } else {
         const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + row;
-        *reinterpret_cast<float4*>(p.partial + at * D + d) = acc;
-        if (d == 0) *reinterpret_cast<float2*>(p.partial_ml + at * 2) = make_float2(mm, ll);
+        *partial_at<D, R>(p, at, d) = acc;
+        if (d == 0) *partial_ml_at<R>(p, at) = make_float2(mm, ll);
       }
     }
     __syncthreads();
@@ -727,7 +754,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   int b, item, c0, pieces;
   if constexpr (kList) {
     rows_done();
-    const int4 cut = p.cut[blockIdx.x / (R / RC)];
+    const int4 cut = *cut_at(p, blockIdx.x / (R / RC));
     if (cut.w == 0) return;
     b = cut.x, item = cut.y, c0 = cut.z, pieces = cut.w;
     s = span_of(p, b);
@@ -760,7 +787,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   };
   float m = -INFINITY, l = 0.0f;
   for (int i = threadIdx.x / RC; i < pieces; i += 32 * kJoinWarps / RC) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + (at(i) + threadIdx.x % RC) * 2);
+    const float2 ml = *partial_ml_at<R>(p, at(i) + threadIdx.x % RC);
     add(m, l, ml.x, ml.y);
   }
 #pragma unroll
@@ -783,13 +810,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
     const bool have = i < pieces;
     const long long row0 = at(have ? i : 0);
     // weight of row lane % RC of this lane's piece (D = 64: a warp has two)
-    const float mi = p.partial_ml[(row0 + lane % RC) * 2];
+    const float mi = partial_ml_at<R>(p, row0 + lane % RC)->x;
     const float z = !have ? 0.0f : (mi == m ? 1.0f : exp2_approx(mi - m));
 #pragma unroll
     for (int r = 0; r < RC; ++r) {
       const float zr = __shfl_sync(0xFFFFFFFFu, z, (lane / kLanes * kLanes + r) & 31);
       if (have) {
-        const float4 v = *reinterpret_cast<const float4*>(p.partial + (row0 + r) * D + 4 * el);
+        const float4 v = *partial_at<D, R>(p, row0 + r, 4 * el);
         acc[r].x += zr * v.x, acc[r].y += zr * v.y, acc[r].z += zr * v.z, acc[r].w += zr * v.w;
       }
     }
@@ -797,7 +824,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
 #pragma unroll
   for (int r = 0; r < RC; ++r) acc_s[stripe][r][el] = acc[r];
   __syncthreads();
-  const float vS = p.a.c.v_S[h];
+  const float vS = head_S(p, p.a.c.v_S, h);
   // (RC kLanes is a multiple of 32 or less than a warp's worth: warp 0 alone)
   for (int i = threadIdx.x; i < (RC * kLanes + 31) / 32 * 32; i += 32 * kJoinWarps) {
     const int r = i / kLanes, e = i % kLanes;

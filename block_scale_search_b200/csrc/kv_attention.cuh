@@ -112,11 +112,30 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Params& p, int b) {
   Span s;
-  const int lo = p.a.q_offsets[b], hi = p.a.q_offsets[b + 1];
+  auto offset = [&](int i) {
+    return *checked(p.a.q_offsets + i, p.a.q_offsets, (static_cast<int64_t>(p.a.batch) + 1) * 4, kSiteKvOffsets);
+  };
+  const int lo = offset(b), hi = offset(b + 1);
   s.q0 = min(max(lo, 0), p.a.total_q);
   s.lq = min(min(max(hi, s.q0), p.a.total_q) - s.q0, p.a.max_q);
-  s.lk = min(max(p.a.kv_lengths[b], 0), p.a.max_kv);
+  s.lk = min(max(*checked(p.a.kv_lengths + b, p.a.kv_lengths, static_cast<int64_t>(p.a.batch) * 4, kSiteKvOffsets), 0),
+             p.a.max_kv);
   return s;
+}
+
+// Entry i of a sequence's row of the page table.
+__device__ __forceinline__ int table_entry(const Params& p, const int* row, int i) {
+  const int64_t pages = (static_cast<int64_t>(p.a.max_kv) + p.a.c.page_size - 1) / p.a.c.page_size;
+  return *checked(row + i, p.a.table, ((p.a.batch - 1) * p.a.table_stride + pages) * 4, kSiteKvTable);
+}
+// 8 elements of a query row, from its element d on.
+__device__ __forceinline__ uint4 query_piece(const Params& p, const uint16_t* at) {
+  return *checked(reinterpret_cast<const uint4*>(at), p.a.Q,
+                  rows_extent(p.a.total_q, p.a.q_token_stride, p.a.q_heads, p.a.q_head_stride, p.a.c.head_dim, 2),
+                  kSiteKvRowsIn);
+}
+__device__ __forceinline__ float head_S(const Params& p, const float* S, int h) {
+  return *checked(S + h, S, p.a.c.kv_heads * 4, kSiteKvS);
 }
 
 // Tokens [lo, hi) that row `row` of a sequence (query row / G, head h G + row % G)
@@ -144,13 +163,15 @@ __device__ __forceinline__ void write_row(const Params& p, const Span& s, int h,
     w.x = pack_f16x2(v.x * inv, v.y * inv);
     w.y = pack_f16x2(v.z * inv, v.w * inv);
   }
-  *reinterpret_cast<uint2*>(o) = w;
+  *checked(reinterpret_cast<uint2*>(o), p.a.out,
+           rows_extent(p.a.total_q, p.a.o_token_stride, p.a.q_heads, p.a.o_head_stride, p.a.c.head_dim, 2), kSiteKvRowsOut) = w;
 }
 
 __device__ __forceinline__ void write_lse(const Params& p, const Span& s, int h, int row, float m, float l) {
   if (p.a.lse == nullptr) return;
   const int64_t t = s.q0 + row / p.group;
-  p.a.lse[t * p.a.q_heads + h * p.group + row % p.group] =
+  *checked(p.a.lse + t * p.a.q_heads + h * p.group + row % p.group, p.a.lse,
+           static_cast<int64_t>(p.a.total_q) * p.a.q_heads * 4, kSiteKvLse) =
       l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 

@@ -217,13 +217,20 @@ __device__ __forceinline__ bool locate(const nvfp4_kv_cache& c, int page_shift, 
 constexpr int kAppendUnroll = 2, kReadUnroll = 8;
 constexpr int kAppendCtas = 4, kReadCtas = 3;
 
+// Bytes of a group, for the checks of its address.
+template <int kBytes>
+struct Group {
+  char bytes[kBytes];
+};
+
 template <int kType>
 __global__ void __launch_bounds__(kThreads, kAppendCtas)
 kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens,
                  const int64_t* __restrict__ slots, int* __restrict__ status) {
   for_groups<kAppendUnroll>(c, m, tokens, [&](const int64_t(&ts)[kAppendUnroll], bool isv, uint32_t h, uint32_t g) {
     const KvRows& X = isv ? V : K;
-    const HeadScale S = head_scale((isv ? c.v_S : c.k_S)[h]);
+    const float* const all_S = isv ? c.v_S : c.k_S;
+    const HeadScale S = head_scale(*checked(all_S + h, all_S, c.kv_heads * 4, kSiteKvS));
     uint8_t* const codes_out = isv ? c.v_codes : c.k_codes;
     uint8_t* const scales_out = isv ? c.v_scales : c.k_scales;
     int64_t slot[kAppendUnroll];
@@ -231,9 +238,14 @@ kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens
     bool finite[kAppendUnroll];
 #pragma unroll
     for (int i = 0; i < kAppendUnroll; ++i) {
-      slot[i] = ts[i] >= 0 ? slots[ts[i]] : -1;
+      slot[i] = ts[i] >= 0 ? *checked(slots + ts[i], slots, tokens * 8, kSiteKvSlots) : -1;
       const int64_t at = (ts[i] < 0 ? 0 : ts[i]) * X.token_stride + h * X.head_stride + 16 * g;
-      finite[i] = load_group<kType>(static_cast<const char*>(X.p) + at * (kType == kFp32 ? 4 : 2), x[i], amax[i]);
+      constexpr int kSize = kType == kFp32 ? 4 : 2;
+      const int64_t bytes = rows_extent(tokens, X.token_stride, c.kv_heads, X.head_stride, c.head_dim, kSize);
+      finite[i] = load_group<kType>(
+          checked(reinterpret_cast<const Group<16 * kSize>*>(static_cast<const char*>(X.p) + at * kSize), X.p, bytes,
+                  kSiteKvRowsIn),
+          x[i], amax[i]);
     }
 #pragma unroll
     for (int i = 0; i < kAppendUnroll; ++i) {
@@ -243,9 +255,10 @@ kv_append_kernel(nvfp4_kv_cache c, KvRows K, KvRows V, Columns m, int64_t tokens
       if (finite[i])
         quantize_group(x[i], amax[i], S, codes, scale);
       else if (status)
-        *status = NVFP4_ERR_NONFINITE;
-      *reinterpret_cast<uint2*>(codes_out + co) = make_uint2(codes[0], codes[1]);
-      scales_out[so] = static_cast<uint8_t>(scale);
+        *checked(status, status, 4, kSiteKvStatus) = NVFP4_ERR_NONFINITE;
+      *checked(reinterpret_cast<uint2*>(codes_out + co), codes_out, codes_extent(c), kSiteKvCodes) =
+          make_uint2(codes[0], codes[1]);
+      *checked(scales_out + so, scales_out, scales_extent(c), kSiteKvScales) = static_cast<uint8_t>(scale);
     }
   });
 }
@@ -266,22 +279,23 @@ kv_read_kernel(nvfp4_kv_cache c, Columns m, int64_t tokens, const int64_t* __res
                void* __restrict__ V) {
   constexpr int kSize = kType == kFp32 ? 4 : 2;
   for_groups<kReadUnroll>(c, m, tokens, [&](const int64_t(&ts)[kReadUnroll], bool isv, uint32_t h, uint32_t g) {
-    const float S = (isv ? c.v_S : c.k_S)[h];
+    const float* const all_S = isv ? c.v_S : c.k_S;
+    const float S = *checked(all_S + h, all_S, c.kv_heads * 4, kSiteKvS);
     const uint8_t* const codes_in = isv ? c.v_codes : c.k_codes;
     const uint8_t* const scales_in = isv ? c.v_scales : c.k_scales;
     int64_t slot[kReadUnroll];
     uint2 w[kReadUnroll];
     uint32_t sc[kReadUnroll];
 #pragma unroll
-    for (int i = 0; i < kReadUnroll; ++i) slot[i] = ts[i] >= 0 ? slots[ts[i]] : -1;
+    for (int i = 0; i < kReadUnroll; ++i) slot[i] = ts[i] >= 0 ? *checked(slots + ts[i], slots, tokens * 8, kSiteKvSlots) : -1;
 #pragma unroll
     for (int i = 0; i < kReadUnroll; ++i) {
       int64_t co, so;
       w[i] = make_uint2(0u, 0u);
       sc[i] = 0;
       if (locate(c, m.page_shift, slot[i], h, g, co, so)) {
-        w[i] = *reinterpret_cast<const uint2*>(codes_in + co);
-        sc[i] = scales_in[so];
+        w[i] = *checked(reinterpret_cast<const uint2*>(codes_in + co), codes_in, codes_extent(c), kSiteKvCodes);
+        sc[i] = *checked(scales_in + so, scales_in, scales_extent(c), kSiteKvScales);
       }
     }
 #pragma unroll
@@ -289,8 +303,10 @@ kv_read_kernel(nvfp4_kv_cache c, Columns m, int64_t tokens, const int64_t* __res
       if (ts[i] < 0) continue;
       uint32_t hh;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hh) : "h"(static_cast<uint16_t>(sc[i] | (sc[i] << 8))));
-      char* const out = static_cast<char*>(isv ? V : K) +
-                        ((ts[i] * c.kv_heads + h) * c.head_dim + 16 * g) * kSize;
+      char* const rows = static_cast<char*>(isv ? V : K);
+      char* const out = reinterpret_cast<char*>(
+          checked(reinterpret_cast<Group<16 * kSize>*>(rows + ((ts[i] * c.kv_heads + h) * c.head_dim + 16 * g) * kSize),
+                  rows, tokens * c.kv_heads * c.head_dim * kSize, kSiteKvRowsOut));
       uint32_t r[16];
       const uint32_t words[2] = {w[i].x, w[i].y};
 #pragma unroll
@@ -343,23 +359,26 @@ kv_copy_kernel(nvfp4_kv_cache c, int64_t code_layer_stride, int64_t scale_layer_
   const int64_t cv = rows * c.head_dim / 32, sv = rows * c.head_dim / 256;  // 16-byte vectors
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int64_t src = pairs.p[i].x, dst = pairs.p[i].y;
-    auto move = [&](uint8_t* base, int64_t layer_stride, int64_t page_stride, int64_t vecs) {
-      const uint4* s = reinterpret_cast<const uint4*>(base + layer * layer_stride + src * page_stride);
-      uint4* d = reinterpret_cast<uint4*>(base + layer * layer_stride + dst * page_stride);
+    auto move = [&](uint8_t* all, int64_t layer_stride, int64_t page_stride, int64_t vecs, int site) {
+      uint8_t* const base = all + layer * layer_stride;
+      const int64_t bytes = site == kSiteKvCodes ? codes_extent(c) : scales_extent(c);
+      const uint4* const s = reinterpret_cast<const uint4*>(base + src * page_stride);
+      uint4* const d = reinterpret_cast<uint4*>(base + dst * page_stride);
+      auto in_base = [&](auto* p) { return checked(p, base, bytes, site); };
       int64_t v = threadIdx.x;
       for (; v + 3 * kThreads < vecs; v += 4 * kThreads) {
         uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = ld_stream_v4(s + v + u * kThreads);
+        for (int u = 0; u < 4; ++u) x[u] = ld_stream_v4(in_base(s + v + u * kThreads));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) d[v + u * kThreads] = x[u];
+        for (int u = 0; u < 4; ++u) *in_base(d + v + u * kThreads) = x[u];
       }
-      for (; v < vecs; v += kThreads) d[v] = ld_stream_v4(s + v);
+      for (; v < vecs; v += kThreads) *in_base(d + v) = ld_stream_v4(in_base(s + v));
     };
-    move(c.k_codes, code_layer_stride, c.code_page_stride, cv);
-    move(c.v_codes, code_layer_stride, c.code_page_stride, cv);
-    move(c.k_scales, scale_layer_stride, c.scale_page_stride, sv);
-    move(c.v_scales, scale_layer_stride, c.scale_page_stride, sv);
+    move(c.k_codes, code_layer_stride, c.code_page_stride, cv, kSiteKvCodes);
+    move(c.v_codes, code_layer_stride, c.code_page_stride, cv, kSiteKvCodes);
+    move(c.k_scales, scale_layer_stride, c.scale_page_stride, sv, kSiteKvScales);
+    move(c.v_scales, scale_layer_stride, c.scale_page_stride, sv, kSiteKvScales);
   }
 }
 

@@ -12,9 +12,39 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "checks.cuh"
 #include "nvfp4hs.h"
 
 namespace nvfp4 {
+
+// Where a check of the checked build failed (checks.cuh): every global address
+// of the cache's kernels goes through checked() or checked_at().
+enum KvCheckSite : int {
+  kSiteKvRowsIn = 64, kSiteKvRowsOut, kSiteKvSlots, kSiteKvStatus, kSiteKvCodes, kSiteKvScales, kSiteKvS,
+  kSiteKvOffsets, kSiteKvTable, kSiteKvLse, kSiteKvPartial, kSiteKvCut, kSiteKvSplit
+};
+
+// Bytes of one layer's codes and scales, from the first page to the last one's end.
+__device__ __forceinline__ int64_t codes_extent(const nvfp4_kv_cache& c) {
+  return (c.num_pages - 1) * c.code_page_stride + static_cast<int64_t>(c.kv_heads) * c.page_size * (c.head_dim / 2);
+}
+__device__ __forceinline__ int64_t scales_extent(const nvfp4_kv_cache& c) {
+  return (c.num_pages - 1) * c.scale_page_stride + static_cast<int64_t>(c.kv_heads) * c.page_size * (c.head_dim / 16);
+}
+// Bytes of strided rows [tokens][heads][dim] of elements of `size` bytes.
+__device__ __forceinline__ int64_t rows_extent(int64_t tokens, int64_t token_stride, int heads, int64_t head_stride,
+                                               int dim, int size) {
+  return ((tokens - 1) * token_stride + (heads - 1) * head_stride + dim) * size;
+}
+// checked() of a T at `at` + kSkip, for addresses kept as integers: what to use as `at`.
+template <typename T, int kSkip = 0>
+__device__ __forceinline__ uint64_t checked_at(uint64_t at, const void* base, int64_t bytes, int site) {
+#ifdef NVFP4HS_CHECKS
+  return reinterpret_cast<uint64_t>(checked(reinterpret_cast<const T*>(at + kSkip), base, bytes, site)) - kSkip;
+#else
+  return at;
+#endif
+}
 
 // A row's element type of the calls that take several.
 enum : int { kBf16 = NVFP4_TYPE_BF16, kFp16 = NVFP4_TYPE_FP16, kFp32 = NVFP4_TYPE_FP32 };

@@ -243,6 +243,18 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (piece >> 3) * kHalfTile + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
+// A row's sums of one split from element d on, and its maximum and sum.
+__device__ __forceinline__ int64_t split_rows(const Params& p) {
+  return static_cast<int64_t>(p.row_blocks) * p.a.batch * p.a.c.kv_heads * p.splits * kRows;
+}
+template <int D>
+__device__ __forceinline__ float4* split_o_at(const Params& p, int64_t row, int d) {
+  return checked(reinterpret_cast<float4*>(p.split_o + row * D + d), p.split_o, split_rows(p) * D * 4, kSiteKvSplit);
+}
+__device__ __forceinline__ float2* split_ml_at(const Params& p, int64_t row) {
+  return checked(p.split_ml + row, p.split_ml, split_rows(p) * 8, kSiteKvSplit);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __grid_constant__ Params p) {
   using L = Layout<D>;
@@ -332,14 +344,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       float mx = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        v[i] = have ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        v[i] = have ? query_piece(p, src + 8 * i) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           mx = fmaxf(mx, fmaxf(fabsf(to_f32(w[j] & 0xFFFFu, p.a.type)), fabsf(to_f32(w[j] >> 16, p.a.type))));
       }
       float shrink;
-      row_scale(mx, p.scale_log2 * c.k_S[h], shrink, f);
+      row_scale(mx, p.scale_log2 * head_S(p, c.k_S, h), shrink, f);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     // needed), loaded a step before it is looked at
     auto page_of = [&](int i) {
       const int tok = (first + i) * kTokens + 16 * lane;
-      return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : 0;
+      return lane < 8 && i < steps && tok < s.lk ? table_entry(p, row_table, tok >> p.page_shift) : 0;
     };
     int page = 0;
     // what is added to a score (-m; 0 while nothing was seen), what the sum may
@@ -478,22 +490,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     if (*reinterpret_cast<volatile int*>(&sh.nan_v) && have) {
       const int tk1 = min(vhi, (first + steps) * kTokens);
       for (int tk = max(vlo, first * kTokens); tk < tk1; ++tk) {
-        const int id = row_table[tk >> p.page_shift];
+        const int id = table_entry(p, row_table, tk >> p.page_shift);
         if (id < 0 || id >= c.num_pages) continue;
         const uint8_t* sc = c.v_scales + id * c.scale_page_stride +
                             (static_cast<int64_t>(h) * c.page_size + (tk & (c.page_size - 1))) * (D / 16);
-        for (int i = 0; i < D / 16; ++i) nan_blocks |= (sc[i] & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t code = *checked(sc + i, c.v_scales, scales_extent(c), kSiteKvScales);
+          nan_blocks |= (code & 0x7Fu) == 0x7Fu ? 1u << i : 0u;
+        }
       }
     }
     float m = at_m();
     // No number of an unfinished phase leaves the CTA as a result.
     if (*reinterpret_cast<volatile int*>(&sh.gave_up)) m = l = __uint_as_float(0x7FC00000u);
     if (m == -INFINITY) l = 0.0f;  // saw no token (the sum may hold some 2^-126)
-    const float inv = l == 0.0f ? 0.0f : c.v_S[h] / l;
+    const float inv = l == 0.0f ? 0.0f : head_S(p, c.v_S, h) / l;
     const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + t) * kTileRows + (threadIdx.x & 127);
     if (p.splits > 1 && have) {
       // (a NaN maximum goes into the sum: the joining maximum passes over it)
-      p.split_ml[at] = m != m ? make_float2(0.0f, m) : make_float2(m, l);
+      *split_ml_at(p, at) = m != m ? make_float2(0.0f, m) : make_float2(m, l);
     }
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
@@ -512,8 +527,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
         if (p.splits > 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(p.split_o + at * D + 32 * q + 4 * j) =
-                make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            *split_o_at<D>(p, at, 32 * q + 4 * j) =
+                make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                            __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -552,12 +568,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     const uint32_t packed = smem_a + L::kPacked;
     auto page_of = [&](int i) {  // lane l < 8: the table's entry for tokens 16 l .. of step i, or -1
       const int tok = (first + i) * kTokens + 16 * lane;
-      return lane < 8 && i < steps && tok < s.lk ? row_table[tok >> p.page_shift] : -1;
+      return lane < 8 && i < steps && tok < s.lk ? table_entry(p, row_table, tok >> p.page_shift) : -1;
     };
     // starts the copy of K or V of step i, whose pages are `ids`, to a slot;
     // returns bit j: the row of piece j is a cached token (the others are any
     // row, to be given scale 0)
-    auto request = [&](int i, int ids, uint64_t codes, uint64_t scales, uint32_t slot) {
+    auto request = [&](int i, int ids, bool isv, uint32_t slot) {
+      const uint64_t codes = isv ? v_codes : k_codes, scales = isv ? v_scales : k_scales;
       uint32_t there = 0;
       if (i < steps) {
 #pragma unroll
@@ -568,9 +585,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
           const uint64_t page = static_cast<uint32_t>(ok ? id : 0);
           const uint32_t in_page = tok & (c.page_size - 1);
           there |= ok ? 1u << j : 0u;
-          copy_async<16>(packed + slot + (j * 128 + th) * 16, codes + page * code_page + in_page * (D / 2));
+          copy_async<16>(packed + slot + (j * 128 + th) * 16,
+                         checked_at<uint4>(codes + page * code_page + in_page * (D / 2), isv ? c.v_codes : c.k_codes,
+                                           codes_extent(c), kSiteKvCodes));
           copy_async<4>(packed + slot + kTokens * (D / 2) + (j * 128 + th) * 4,
-                        scales + page * scale_page + in_page * (D / 16));
+                        checked_at<uint32_t>(scales + page * scale_page + in_page * (D / 16),
+                                             isv ? c.v_scales : c.k_scales, scales_extent(c), kSiteKvScales));
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -622,8 +642,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       fence_async();
     };
     int ids = page_of(0);
-    uint32_t there = request(0, ids, k_codes, k_scales, 0);
-    request(0, ids, v_codes, v_scales, L::kSlot);
+    uint32_t there = request(0, ids, false, 0);
+    request(0, ids, true, L::kSlot);
     ids = page_of(1);
     uint32_t slot = 0;  // of K of step i; V's is the next, and the one after is free
     auto after = [](uint32_t sl) { return sl == 2 * L::kSlot ? 0u : sl + L::kSlot; };
@@ -631,10 +651,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
       const int st = i & 1;
       const uint32_t parity = ((i >> 1) & 1) ^ 1, v_slot = after(slot), free_slot = after(v_slot);
       const int ids_after = page_of(i + 2);
-      const uint32_t next_there = request(i + 1, ids, k_codes, k_scales, free_slot);
+      const uint32_t next_there = request(i + 1, ids, false, free_slot);
       decode(slot, there, false, kKEmpty + st, parity, smem + L::kK + st * L::kTile);
       mbar_arrive(bar(kKFull + st));
-      request(i + 1, ids, v_codes, v_scales, slot);
+      request(i + 1, ids, true, slot);
       decode(v_slot, there, true, kVEmpty + st, parity, smem + L::kV + st * L::kTile);
       mbar_arrive(bar(kVFull + st));
       ids = ids_after;
@@ -745,7 +765,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __
   const int rows = s.lq * p.group, row = rb * kRows + in_item;
   if (rows <= p.rows_limit || row >= rows) return;
   auto at = [&](int split) { return (static_cast<int64_t>(item) * p.splits + split) * kRows + in_item; };
-  const float2 ml = lane < p.splits ? p.split_ml[at(lane)] : make_float2(-INFINITY, 0.0f);
+  const float2 ml = lane < p.splits ? *split_ml_at(p, at(lane)) : make_float2(-INFINITY, 0.0f);
   float m = ml.x;
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __
     const int i = i0 + half;
     const float zi = __shfl_sync(0xFFFFFFFFu, z, i & 31);
     if (i < p.splits && (saw >> i) & 1) {
-      const float4 v = *reinterpret_cast<const float4*>(p.split_o + at(i) * D + 4 * el);
+      const float4 v = *split_o_at<D>(p, at(i), 4 * el);
       acc.x += zi * v.x, acc.y += zi * v.y, acc.z += zi * v.z, acc.w += zi * v.w;
     }
   }
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_prompt_join_kernel(const __
     acc.z += __shfl_xor_sync(0xFFFFFFFFu, acc.z, 16);
     acc.w += __shfl_xor_sync(0xFFFFFFFFu, acc.w, 16);
   }
-  if (half == 0) write_row(p, s, h, row, 4 * el, acc, l == 0.0f ? 0.0f : p.a.c.v_S[h] / l);
+  if (half == 0) write_row(p, s, h, row, 4 * el, acc, l == 0.0f ? 0.0f : head_S(p, p.a.c.v_S, h) / l);
   if (lane == 0) write_lse(p, s, h, row, m, l);
 }
 

@@ -64,8 +64,8 @@ int nvfp4_version(void);
 
 /* Bounds checks (debugging aid; no counterpart on the pages).  A library built
  * with -DNVFP4HS_CHECKS checks every global-memory address of the per-step
- * kernels (diagonal Hessian, global scale, sweep, dequantize) against the
- * extent of its buffer that the call's size arguments imply; an address
+ * kernels (diagonal Hessian, global scale, sweep, dequantize) and of the K/V
+ * cache's against the extent of its buffer that the call's size arguments imply; an address
  * outside is counted, the first is recorded, and the access goes to a dummy
  * buffer instead (no fault, no write to memory the call does not own).
  * nvfp4_debug_checks_compiled() is 1 in such a build, 0 otherwise.

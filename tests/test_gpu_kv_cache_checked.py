@@ -1,5 +1,6 @@
-"""The K/V cache under the bounds-checked build of the library, on a B200: a wait
-that runs out leaves NaN and a count, never a number."""
+"""The K/V cache under the bounds-checked build of the library, on a B200: no
+address outside a buffer, and a wait that runs out leaves NaN and a count, never
+a number."""
 import os
 import subprocess
 import sys
@@ -72,3 +73,14 @@ def test_the_normal_build_keeps_its_limit():
         pytest.skip("checked build")
     with pytest.raises(nv.NVFP4Error):
         nv.nvfp4_debug_kv_wait_limit(0)
+
+
+def test_the_cache_touches_nothing_outside_its_buffers():
+    """Every global address of append, read, copy and attention against its buffer's extent."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    cmd = [sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider",
+           os.path.join(here, "test_gpu_kv_cache.py"), os.path.join(here, "test_gpu_kv_cache_edges.py")]
+    out = subprocess.run(cmd, cwd=ROOT, env=checked_env(), capture_output=True, text=True, timeout=900)
+    tail = out.stdout[-3000:] + out.stderr[-2000:]
+    assert out.returncode == 0, tail
+    assert "bounds checks: 0 failed" in out.stdout, tail
