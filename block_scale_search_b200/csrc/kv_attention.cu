@@ -489,186 +489,197 @@ kv_rows_kernel(const __grid_constant__ Params p) {
     auto tok = [](int r) { return r ^ ((r >> 1) & 1); };
 
     int use = 0;  // ring position of the tile in use, in bytes
-    for (int k = 0; k < mine; ++k) {
-      const uint32_t none = none_next;
-      request();
-      copy_wait<kStages - 1>();
-      __syncwarp();
-      const uint8_t* const stage = ring + use;
-      use = kStageBytes - use;
-      const int tb = (s.t0 + ts + warp + k * kWarps) * kTile;  // first token
-      const bool edge = tb < all_lo || tb + kTile > all_hi || none != 0;
-      // ---- S^T
-      float x[NT][2][4] = {};
-      uint32_t kw[2][2][KW];
-      uint32_t ksc[2][2];  // two scales (D = 64: one, and a zero)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint8_t* const kc = stage + half * kHalfBytes;
-        const uint8_t* const ks = kc + kCodes;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = tok(g) + 8 * j;
-          uint32_t(&k4)[KW] = kw[half][j];
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kc + t * 64 + l4 * 16);
-            k4[0] = v.x, k4[1] = v.y, k4[2] = v.z, k4[3] = v.w;
-            ksc[half][j] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + t * 8 + l4 * 2));
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kc + t * 32 + l4 * 8);
-            k4[0] = v.x, k4[1] = v.y;
-            ksc[half][j] = e4m3x2_to_f16x2(ks[t * 4 + l4]);
-          }
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        uint4 qw[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) qw[n] = q[(n * KW + w) * 32];
-        const uint32_t sel = w < 2 ? 0x1010 : 0x3232;  // block of word w: two words a block
+    auto walk = [&](auto hold) {
+      for (int k = 0; k < mine; ++k) {
+        const uint32_t none = none_next;
+        request();
+        copy_wait<kStages - 1>();
+        __syncwarp();
+        const uint8_t* const stage = ring + use;
+        use = kStageBytes - use;
+        const int tb = (s.t0 + ts + warp + k * kWarps) * kTile;  // first token
+        const bool edge = tb < all_lo || tb + kTile > all_hi || none != 0;
+        // ---- S^T
+        float x[NT][2][4] = {};
+        uint32_t kw[2][2][KW];
+        uint32_t ksc[2][2];  // two scales (D = 64: one, and a zero)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t s0 = __byte_perm(ksc[half][0], 0, sel), s1 = __byte_perm(ksc[half][1], 0, sel);
-          uint32_t e0[4], e1[4];
-          e2m1x8_to_f16x2(kw[half][0][w], e0);
-          e2m1x8_to_f16x2(kw[half][1][w], e1);
-          const uint32_t a[4] = {mul_f16x2(e0[0], s0), mul_f16x2(e1[0], s1), mul_f16x2(e0[1], s0), mul_f16x2(e1[1], s1)};
-          const uint32_t b[4] = {mul_f16x2(e0[2], s0), mul_f16x2(e1[2], s1), mul_f16x2(e0[3], s0), mul_f16x2(e1[3], s1)};
+          const uint8_t* const kc = stage + half * kHalfBytes;
+          const uint8_t* const ks = kc + kCodes;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma(x[n][half], a, qw[n].x, qw[n].y);
-            mma(x[n][half], b, qw[n].z, qw[n].w);
+          for (int j = 0; j < 2; ++j) {
+            const int t = tok(g) + 8 * j;
+            uint32_t(&k4)[KW] = kw[half][j];
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kc + t * 64 + l4 * 16);
+              k4[0] = v.x, k4[1] = v.y, k4[2] = v.z, k4[3] = v.w;
+              ksc[half][j] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + t * 8 + l4 * 2));
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(kc + t * 32 + l4 * 8);
+              k4[0] = v.x, k4[1] = v.y;
+              ksc[half][j] = e4m3x2_to_f16x2(ks[t * 4 + l4]);
+            }
           }
         }
-      }
-      if (edge) {
-        __syncwarp();  // keeps this a branch
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int w = 0; w < KW; ++w) {
+          uint4 qw[NT];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = tb + (i >> 2) * kHalf + tok(g) + (i & 2) * 4;
-            if (t < vlo[n][i & 1] || t >= vhi[n][i & 1] || ((none >> (i >> 2)) & 1)) x[n][i >> 2][i & 3] = -INFINITY;
+          for (int n = 0; n < NT; ++n) qw[n] = q[(n * KW + w) * 32];
+          const uint32_t sel = w < 2 ? 0x1010 : 0x3232;  // block of word w: two words a block
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t s0 = __byte_perm(ksc[half][0], 0, sel), s1 = __byte_perm(ksc[half][1], 0, sel);
+            uint32_t e0[4], e1[4];
+            e2m1x8_to_f16x2(kw[half][0][w], e0);
+            e2m1x8_to_f16x2(kw[half][1][w], e1);
+            const uint32_t a[4] = {mul_f16x2(e0[0], s0), mul_f16x2(e1[0], s1), mul_f16x2(e0[1], s0), mul_f16x2(e1[1], s1)};
+            const uint32_t b[4] = {mul_f16x2(e0[2], s0), mul_f16x2(e1[2], s1), mul_f16x2(e0[3], s0), mul_f16x2(e1[3], s1)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma(x[n][half], a, qw[n].x, qw[n].y);
+              mma(x[n][half], b, qw[n].z, qw[n].w);
+            }
           }
-      }
-      bool over = false;
+        }
+        if (edge) {
+          __syncwarp();  // keeps this a branch
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          over |= fmaf(fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])), f[n][i],
-                       down[n][i]) > limit[n][i];
-      }
-      if (__any_sync(0xFFFFFFFFu, over)) {
+            for (int i = 0; i < 8; ++i) {
+              const int t = tb + (i >> 2) * kHalf + tok(g) + (i & 2) * 4;
+              if (t < vlo[n][i & 1] || t >= vhi[n][i & 1] || ((none >> (i >> 2)) & 1)) x[n][i >> 2][i & 3] = -INFINITY;
+            }
+        }
+        bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])) * f[n][i];
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-            const float m = at_m(n, i);
-            t = fmaxf(t - kAim, m);
-            const float r = t == m ? 1.0f : exp2_approx(m - t);
-            if (t != -INFINITY) down[n][i] = -t, limit[n][i] = kTop;
-            l[n][i] *= r;
+          for (int i = 0; i < 2; ++i)
+            over |= fmaf(fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])), f[n][i],
+                         down[n][i]) > limit[n][i];
+        }
+        if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-            for (int u = 0; u < VW * 4; ++u) o[n][u][i] *= r, o[n][u][i + 2] *= r;
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float t = m_for(fmaxf(fmaxf(x[n][0][i], x[n][0][i + 2]), fmaxf(x[n][1][i], x[n][1][i + 2])), f[n][i]);
+              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+              const float m = at_m(n, i);
+              t = fmaxf(t, m);
+              const float r = t == m ? 1.0f : exp2_approx(m - t);
+              if (t != -INFINITY) down[n][i] = -t, limit[n][i] = kTop;
+              l[n][i] *= r;
+#pragma unroll
+              for (int u = 0; u < VW * 4; ++u) o[n][u][i] *= r, o[n][u][i + 2] *= r;
+            }
           }
         }
-      }
-      uint32_t pb[NT][2][2];
+        uint32_t pb[NT][2][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float y = fmaf(x[n][half][i], f[n][i & 1], down[n][i & 1]);
+              x[n][half][i] = exp2_approx(decltype(hold)::value ? held(y) : y);
+            }
+            l[n][0] += x[n][half][0] + x[n][half][2];
+            l[n][1] += x[n][half][1] + x[n][half][3];
+            pb[n][half][0] = transpose8x8(pack_f16x2(x[n][half][0], x[n][half][1]));
+            pb[n][half][1] = transpose8x8(pack_f16x2(x[n][half][2], x[n][half][3]));
+          }
+        }
+        // ---- O^T: tokens of the k index 2 l4, 2 l4 + 1, 2 l4 + 8, 2 l4 + 9
+        const int ta = tok(2 * l4), tc = tok(2 * l4 + 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[n][half][i] = exp2_approx(fmaf(x[n][half][i], f[n][i & 1], down[n][i & 1]));
-          l[n][0] += x[n][half][0] + x[n][half][2];
-          l[n][1] += x[n][half][1] + x[n][half][3];
-          pb[n][half][0] = transpose8x8(pack_f16x2(x[n][half][0], x[n][half][1]));
-          pb[n][half][1] = transpose8x8(pack_f16x2(x[n][half][2], x[n][half][3]));
-        }
-      }
-      // ---- O^T: tokens of the k index 2 l4, 2 l4 + 1, 2 l4 + 8, 2 l4 + 9
-      const int ta = tok(2 * l4), tc = tok(2 * l4 + 1);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint8_t* const vc = stage + half * kHalfBytes + kCodes + kScales;
-        const uint8_t* const vs = vc + kCodes;
-        uint32_t vw[4][VW], vsc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = (j & 1 ? tc : ta) + (j & 2) * 4;
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(vc + t * 64 + g * 8);
-            vw[j][0] = v.x, vw[j][1] = v.y;
-            vsc[j] = vs[t * 8 + g];
-          } else {
-            vw[j][0] = *reinterpret_cast<const uint32_t*>(vc + t * 32 + g * 4);
-            vsc[j] = vs[t * 4 + (g >> 1)];
-          }
-        }
-        uint32_t nan_tokens = 0;  // bit j: vsc[j] is NaN and its token may be hidden from some row
-        if (edge) {
-          __syncwarp();
+          const uint8_t* const vc = stage + half * kHalfBytes + kCodes + kScales;
+          const uint8_t* const vs = vc + kCodes;
+          uint32_t vw[4][VW], vsc[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int t = tb + half * kHalf + (j & 1 ? tc : ta) + (j & 2) * 4;
-            const bool gone = t >= s.lk || ((none >> half) & 1);
-            if (gone || (vsc[j] & 0x7Fu) == 0x7Fu) {
-              // 0 * NaN would reach rows that do not see the token: take it
-              // out of the product and give it to the rows that do (below)
-              if (!gone) nan_tokens |= 1u << j;
-              vsc[j] = 0;
+            const int t = (j & 1 ? tc : ta) + (j & 2) * 4;
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(vc + t * 64 + g * 8);
+              vw[j][0] = v.x, vw[j][1] = v.y;
+              vsc[j] = vs[t * 8 + g];
+            } else {
+              vw[j][0] = *reinterpret_cast<const uint32_t*>(vc + t * 32 + g * 4);
+              vsc[j] = vs[t * 4 + (g >> 1)];
             }
           }
-        }
-        const uint32_t sab = e4m3x2_to_f16x2(vsc[0] | (vsc[1] << 8));
-        const uint32_t scd = e4m3x2_to_f16x2(vsc[2] | (vsc[3] << 8));
+          uint32_t nan_tokens = 0;  // bit j: vsc[j] is NaN and its token may be hidden from some row
+          if (edge) {
+            __syncwarp();
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          constexpr uint32_t kLow = 0x0F0F0F0Fu;
-          uint32_t lo_ab[4], hi_ab[4], lo_cd[4], hi_cd[4];
-          e2m1x8_to_f16x2(merge(vw[0][w], vw[1][w] << 4, kLow), lo_ab);
-          e2m1x8_to_f16x2(merge(vw[0][w] >> 4, vw[1][w], kLow), hi_ab);
-          e2m1x8_to_f16x2(merge(vw[2][w], vw[3][w] << 4, kLow), lo_cd);
-          e2m1x8_to_f16x2(merge(vw[2][w] >> 4, vw[3][w], kLow), hi_cd);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a[4] = {mul_f16x2(lo_ab[u], sab), mul_f16x2(hi_ab[u], sab),
-                                   mul_f16x2(lo_cd[u], scd), mul_f16x2(hi_cd[u], scd)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma(o[n][4 * w + u], a, pb[n][half][0], pb[n][half][1]);
-          }
-        }
-        if (edge && __any_sync(0xFFFFFFFFu, nan_tokens != 0)) {
-          // the NaN tokens of lane g's own elements, gathered over l4
-#pragma unroll 1
-          for (int src = 0; src < 4; ++src) {
-            const uint32_t bits = __shfl_sync(0xFFFFFFFFu, nan_tokens, (lane & ~3) | src);
-#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
-              if (!((bits >> j) & 1)) continue;
-              const int t = tb + half * kHalf + tok(2 * src + (j & 1)) + (j & 2) * 4;
+              const int t = tb + half * kHalf + (j & 1 ? tc : ta) + (j & 2) * 4;
+              const bool gone = t >= s.lk || ((none >> half) & 1);
+              if (gone || (vsc[j] & 0x7Fu) == 0x7Fu) {
+                // 0 * NaN would reach rows that do not see the token: take it
+                // out of the product and give it to the rows that do (below)
+                if (!gone) nan_tokens |= 1u << j;
+                vsc[j] = 0;
+              }
+            }
+          }
+          const uint32_t sab = e4m3x2_to_f16x2(vsc[0] | (vsc[1] << 8));
+          const uint32_t scd = e4m3x2_to_f16x2(vsc[2] | (vsc[3] << 8));
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+          for (int w = 0; w < VW; ++w) {
+            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+            uint32_t lo_ab[4], hi_ab[4], lo_cd[4], hi_cd[4];
+            e2m1x8_to_f16x2(merge(vw[0][w], vw[1][w] << 4, kLow), lo_ab);
+            e2m1x8_to_f16x2(merge(vw[0][w] >> 4, vw[1][w], kLow), hi_ab);
+            e2m1x8_to_f16x2(merge(vw[2][w], vw[3][w] << 4, kLow), lo_cd);
+            e2m1x8_to_f16x2(merge(vw[2][w] >> 4, vw[3][w], kLow), hi_cd);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (t >= vlo[n][i] && t < vhi[n][i]) {
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t a[4] = {mul_f16x2(lo_ab[u], sab), mul_f16x2(hi_ab[u], sab),
+                                     mul_f16x2(lo_cd[u], scd), mul_f16x2(hi_cd[u], scd)};
 #pragma unroll
-                    for (int u = 0; u < VW * 4; ++u)
-                      o[n][u][i] = o[n][u][i + 2] = __uint_as_float(0x7FC00000u);
-                  }
+              for (int n = 0; n < NT; ++n) mma(o[n][4 * w + u], a, pb[n][half][0], pb[n][half][1]);
+            }
+          }
+          if (edge && __any_sync(0xFFFFFFFFu, nan_tokens != 0)) {
+            // the NaN tokens of lane g's own elements, gathered over l4
+#pragma unroll 1
+            for (int src = 0; src < 4; ++src) {
+              const uint32_t bits = __shfl_sync(0xFFFFFFFFu, nan_tokens, (lane & ~3) | src);
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) {
+                if (!((bits >> j) & 1)) continue;
+                const int t = tb + half * kHalf + tok(2 * src + (j & 1)) + (j & 2) * 4;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (t >= vlo[n][i] && t < vhi[n][i]) {
+#pragma unroll
+                      for (int u = 0; u < VW * 4; ++u)
+                        o[n][u][i] = o[n][u][i + 2] = __uint_as_float(0x7FC00000u);
+                    }
+              }
             }
           }
         }
+        __syncwarp();  // the stage may be written again
       }
-      __syncwarp();  // the stage may be written again
-    }
+    };
+    bool far = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) far |= may_pass_top<D>(f[n][0]) || may_pass_top<D>(f[n][1]);
+    if (__any_sync(0xFFFFFFFFu, far))
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
 
     // ---- join the warps (their areas lie over all rings)
     __syncthreads();

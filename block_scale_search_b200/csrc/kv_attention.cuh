@@ -17,6 +17,20 @@ namespace nvfp4 {
 // one whose V is 0, spread by a third of a bit, came out 1% off, 82% at 25.5
 // bits; so they are 2^-17 off.)
 constexpr float kAim = 7.0f, kTop = 15.0f;
+// m for the largest score, x f: not above its exact value - kAim, so that P is
+// at least 2^7 there, and at most 2^15 below 2^25, where FP32 steps are 4 or
+// less.  Rows whose scores may lie further out (|q| is below 2^16, |k| at most
+// 6 * 448) have their exponents held at kTop: tokens with the largest score then
+// have equal weights and the others theirs, to what FP32 knows of such scores.
+// Holding takes an instruction a score, so the loops exist with and without.
+__device__ __forceinline__ float m_for(float x, float f) { return __fadd_rd(__fmul_rd(x, f), -kAim); }
+template <int D>
+__device__ __forceinline__ bool may_pass_top(float f) { return !(f < 0x1p25f / (D * 65536.0f * 2688.0f)); }
+__device__ __forceinline__ float held(float y) {
+  float r;  // (a NaN stays)
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kTop));
+  return r;
+}
 
 struct Params {
   KvAttention a;

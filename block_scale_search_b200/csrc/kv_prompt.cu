@@ -31,6 +31,8 @@
 // K and V rows lie alike: 128-byte rows of 64 elements with the 128-byte
 // swizzle, halves of a row 16 KB apart.  K is the K-major operand of S; of
 // P V, whose inner index are the tokens, the same rows are the MN-major one.
+#include <type_traits>
+
 #include "kv_attention.cuh"
 
 namespace nvfp4 {
@@ -384,102 +386,112 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const __gr
     auto at_m = [&] { return limit == -INFINITY ? -INFINITY : -down; };
     const int from = t ? tile_from[1] : tile_from[0], to = t ? tile_to[1] : tile_to[0];
     page = page_of(from);
-    for (int i = from; i < to; ++i) {
-      const uint32_t parity = (i - from) & 1;
-      const int tb = (first + i) * kTokens;
-      const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
-      page = page_of(i + 1);
-      const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
-      mbar_wait<kSoftmaxSleep>(&sh, bar(kSFull + t), parity);
-      tc_fence_after();
-      uint32_t x[4][32];
+    auto walk = [&](auto hold) {
+      for (int i = from; i < to; ++i) {
+        const uint32_t parity = (i - from) & 1;
+        const int tb = (first + i) * kTokens;
+        const uint32_t dead = __ballot_sync(0xFFFFFFFFu, page < 0 || page >= c.num_pages);
+        page = page_of(i + 1);
+        const bool edge = tb < all_lo || tb + kTokens > all_hi || dead != 0;
+        mbar_wait<kSoftmaxSleep>(&sh, bar(kSFull + t), parity);
+        tc_fence_after();
+        uint32_t x[4][32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_load32(s_col + 32 * q, x[q]);
-      tmem_wait_load();
-      if (edge) {  // hidden scores become -inf
-        __syncwarp();  // keeps this a branch
-        // tokens [a, z) of the step are visible but for those of dead pages
-        const int a = min(max(vlo - tb, 0), kTokens), z = min(max(vhi - tb, 0), kTokens);
+        for (int q = 0; q < 4; ++q) tmem_load32(s_col + 32 * q, x[q]);
+        tmem_wait_load();
+        if (edge) {  // hidden scores become -inf
+          __syncwarp();  // keeps this a branch
+          // tokens [a, z) of the step are visible but for those of dead pages
+          const int a = min(max(vlo - tb, 0), kTokens), z = min(max(vhi - tb, 0), kTokens);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // bit j: column 32 q + j is visible
+            const int from = min(max(a - 32 * q, 0), 32), to = min(max(z - 32 * q, 0), 32);
+            uint32_t vis = static_cast<uint32_t>((uint64_t{1} << to) - (uint64_t{1} << from));
+            if (to <= from) vis = 0;
+            if ((dead >> (2 * q)) & 1) vis &= 0xFFFF0000u;
+            if ((dead >> (2 * q + 1)) & 1) vis &= 0x0000FFFFu;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[q][j] = (vis >> j) & 1 ? x[q][j] : 0xFF800000u;
+          }
+        }
+        // a NaN score has to reach m: not every exponential below would keep it
+        float m4[4];  // chains short enough to overlap
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          // bit j: column 32 q + j is visible
-          const int from = min(max(a - 32 * q, 0), 32), to = min(max(z - 32 * q, 0), 32);
-          uint32_t vis = static_cast<uint32_t>((uint64_t{1} << to) - (uint64_t{1} << from));
-          if (to <= from) vis = 0;
-          if ((dead >> (2 * q)) & 1) vis &= 0xFFFF0000u;
-          if ((dead >> (2 * q + 1)) & 1) vis &= 0x0000FFFFu;
+          float a = __uint_as_float(x[q][0]), z = __uint_as_float(x[q][1]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[q][j] = (vis >> j) & 1 ? x[q][j] : 0xFF800000u;
+          for (int j = 2; j < 32; j += 4) {
+            a = max3_nan(a, __uint_as_float(x[q][j]), __uint_as_float(x[q][j + 1]));
+            if (j + 3 < 32) z = max3_nan(z, __uint_as_float(x[q][j + 2]), __uint_as_float(x[q][j + 3]));
+          }
+          m4[q] = max3_nan(a, z, z);
         }
-      }
-      // a NaN score has to reach m: not every exponential below would keep it
-      float m4[4];  // chains short enough to overlap
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a = __uint_as_float(x[q][0]), z = __uint_as_float(x[q][1]);
-#pragma unroll
-        for (int j = 2; j < 32; j += 4) {
-          a = max3_nan(a, __uint_as_float(x[q][j]), __uint_as_float(x[q][j + 1]));
-          if (j + 3 < 32) z = max3_nan(z, __uint_as_float(x[q][j + 2]), __uint_as_float(x[q][j + 3]));
-        }
-        m4[q] = max3_nan(a, z, z);
-      }
-      const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
-      if (__any_sync(0xFFFFFFFFu, !(fmaf(mx, f, down) <= limit))) {
-        // (inf - inf below would be NaN, which the polynomial does not keep)
-        const float m = at_m(), next = mx * f - kAim;
-        float top = max3_nan(m, next, next);
-        if (top == INFINITY) top = __uint_as_float(0x7FC00000u);
-        const float r = top == m ? 1.0f : exp2_approx(m - top);
-        if (top != -INFINITY) down = -top, limit = kTop;
-        l *= r;
-        if (i > from) {
+        const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+        if (__any_sync(0xFFFFFFFFu, !(fmaf(mx, f, down) <= limit))) {
+          // (inf - inf below would be NaN, which the polynomial does not keep)
+          const float m = at_m(), next = m_for(mx, f);
+          float top = max3_nan(m, next, next);
+          if (top == INFINITY) top = __uint_as_float(0x7FC00000u);
+          const float r = top == m ? 1.0f : exp2_approx(m - top);
+          if (top != -INFINITY) down = -top, limit = kTop;
+          l *= r;
+          if (i > from) {
 #pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t o[16];
-            tmem_load16(o_col + 16 * q, o);
-            tmem_wait_load();
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_load16(o_col + 16 * q, o);
+              tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
-            tmem_store16(o_col + 16 * q, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * r);
+              tmem_store16(o_col + 16 * q, o);
+            }
           }
         }
-      }
-      const f32x2_t f2 = f2_pack(f, f), d2 = f2_pack(down, down);
-      f32x2_t sum[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
+        const f32x2_t f2 = f2_pack(f, f), d2 = f2_pack(down, down);
+        f32x2_t sum[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t o[16];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const f32x2_t y = f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2);
+          for (int j = 0; j < 16; ++j) {
+            f32x2_t y = f2_fma(f2_pack(__uint_as_float(x[q][2 * j]), __uint_as_float(x[q][2 * j + 1])), f2, d2);
+            float a, z;
+            if constexpr (decltype(hold)::value) {
+              f2_unpack(y, a, z);
+              y = f2_pack(held(a), held(z));
+            }
+            if (j % kPolyEvery == kPolyEvery - 1) {
+              exp2_poly2(y, a, z);
+            } else {
+              f2_unpack(y, a, z);
+              a = exp2_approx(a);
+              z = exp2_approx(z);
+            }
+            sum[j & 3] = f2_add(sum[j & 3], f2_pack(a, z));
+            o[j] = pack_f16x2(a, z);
+          }
+          tmem_store16(s_col + 16 * q, o);  // over scores that are in registers
+          if (q == 1) {  // P V may begin
+            tmem_wait_store();
+            tc_fence_before();
+            mbar_arrive(bar(kPFull + 2 * t));
+          }
+        }
+        {
           float a, z;
-          if (j % kPolyEvery == kPolyEvery - 1) {
-            exp2_poly2(y, a, z);
-          } else {
-            f2_unpack(y, a, z);
-            a = exp2_approx(a);
-            z = exp2_approx(z);
-          }
-          sum[j & 3] = f2_add(sum[j & 3], f2_pack(a, z));
-          o[j] = pack_f16x2(a, z);
+          f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, z);
+          l += a + z;
         }
-        tmem_store16(s_col + 16 * q, o);  // over scores that are in registers
-        if (q == 1) {  // P V may begin
-          tmem_wait_store();
-          tc_fence_before();
-          mbar_arrive(bar(kPFull + 2 * t));
-        }
+        tmem_wait_store();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + 2 * t + 1));
       }
-      {
-        float a, z;
-        f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, z);
-        l += a + z;
-      }
-      tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(bar(kPFull + 2 * t + 1));
-    }
+    };
+    if (__any_sync(0xFFFFFFFFu, may_pass_top<D>(f)))
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
     // -------------------------------------------------------------- result
     if (to > from) {
       mbar_wait(&sh, bar(kOFull + t), 0);

@@ -209,3 +209,43 @@ def test_weights_far_below_the_largest(nv, lq, dim, bits):
     tol = (w @ v.abs() / L * (2 ** -11 + 2 * d) + n * 2 ** -32 * v.abs().max() / L + o.abs() * 2 ** -8)
     check(out, o, tol, "out")
     check(lse, (m + torch.log(L))[..., 0], (d + (m.abs() + torch.log(L)) * 2 ** -21)[..., 0], "lse")
+
+
+# ---------------------------------------------------------------- large scores
+
+@pytest.mark.parametrize("lq", [1, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bits", [20, 24, 26, 28, 31, 40, 70, 120])
+def test_large_scores(nv, lq, dim, bits):
+    """Largest scores of 2^bits, seen by two tokens; the next ones are a third less, whose weights
+    are 0 in 64 bits.  So out is the mean of two rows of V: both have the same weight, rounded to
+    FP16 (2^-11; its exponent, score - m in FP32, is no whole number), against a sum that is not;
+    2^-20 for sums and quotients, and out's own rounding.  lse: 2^-21 of it, as elsewhere, and the
+    FP32 product of the factors (2^-22)."""
+    gen = torch.Generator().manual_seed(bits)
+    n, heads = 1500, 8
+    pages, table = build_batch(gen, [n], 16)
+    cache = make_cache(nv, gen, pages, 16, 1, dim, scale_lo=0x38, scale_hi=0x39)
+    cache.k_codes[...] = 0
+    cache.k_codes[..., 0] = torch.randint(0, 7, cache.k_codes.shape[:-1], generator=gen, dtype=torch.uint8).to(DEV)
+    top = (700, 1203)
+    for t in top:
+        cache.k_codes[table[0, t // 16], 0, t % 16, 0] = 7
+    cache.k_S.fill_(0.7)
+    Q = torch.zeros(lq, heads, dim)
+    Q[..., 0] = 3.0
+    Q[:, 1::2, 0] = -3.0                               # these heads' largest score is 0
+    Q = Q.to(FP16).to(DEV)
+    scale = 2.0 ** bits / (3.0 * 6.0 * float(cache.k_S[0].double()))
+    out, lse = nv.kv_attention(cache, Q, ints(0, lq), ints(n), table.to(DEV), lq, n, scale, causal=False, want_lse=True)
+    v = decode(cache.v_codes.cpu()[table[0, torch.arange(n) // 16].long(), 0, torch.arange(n) % 16],
+               cache.v_scales.cpu()[table[0, torch.arange(n) // 16].long(), 0, torch.arange(n) % 16], cache.v_S[0])
+    o = ((v[top[0]] + v[top[1]]) / 2).expand(lq, heads // 2, dim)
+    A = ((v[top[0]].abs() + v[top[1]].abs()) / 2).expand(lq, heads // 2, dim)
+    check(out[:, 0::2], o, A * (2 ** -11 + 2 ** -20) + o.abs() * 2 ** -11 + 1e-7, "out")
+    l = torch.full((lq, heads // 2), 2.0 ** bits, dtype=torch.float64)
+    check(lse[:, 0::2], l, l * (2 ** -21 + 2 ** -22), "lse")
+    zero = cache.k_codes.cpu()[table[0, torch.arange(n) // 16].long(), 0, torch.arange(n) % 16, 0] == 0
+    o = v[zero].mean(0).expand(lq, heads // 2, dim)
+    A = v[zero].abs().mean(0).expand(lq, heads // 2, dim)
+    check(out[:, 1::2], o, A * (2 ** -11 + 2 ** -18) + o.abs() * 2 ** -11 + 1e-7, "out of scores 0")
