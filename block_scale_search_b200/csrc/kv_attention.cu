@@ -884,11 +884,12 @@ Plan plan_of(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads, int kv_h
   // without a CTA, a row a CTA shortens the walk over the pieces (two sequences
   // of 131072 tokens, 16 items of 47 pieces: 72 us with 8 rows a CTA, 67 with
   // 1; 48 of 8192: 60 us with 8, 64 with 1).  Where items are many, looking at
-  // all lengths in every CTA costs more than a list of the cut ones (256
-  // sequences of up to 1000 tokens 65 us, with the list 59; 16 of 4100 with 16
-  // rows 17.5 and 18.9).
+  // all lengths in every CTA costs more than a list of the cut ones (8 KV heads
+  // of 128, sequences of up to 1000 tokens, without and with the list: 24
+  // sequences 16.3 and 16.7 us, 48 21.3 and 21.7, 64, which are 512 CTAs, 27.0
+  // and 25.0, 256 74.2 and 67.7; of up to 8000: 24 41.0 and 41.6, 64 94.1 and 91.3).
   const int64_t join_ctas = static_cast<int64_t>(p.items) * batch * p.nt;
-  p.join = join_ctas < num_sms ? Plan::kByRow : (join_ctas <= 512 ? Plan::kByTile : Plan::kListed);
+  p.join = join_ctas < num_sms ? Plan::kByRow : (join_ctas < 512 ? Plan::kByTile : Plan::kListed);
   const double tiles = static_cast<double>(batch) * p.items * static_cast<double>((max_kv + kTile - 1) / kTile + 1 + kItemCost);
   p.fits = tiles < 0x7FF00000;
   const int64_t wave = static_cast<int64_t>(num_sms) * ctas_per_sm(head_dim, p.nt);
