@@ -1018,7 +1018,8 @@ def kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Ten
     """Quantizes rows K, V [tokens, kv_heads, head_dim] (bf16, fp16 or float32; any
     token and head strides that are multiples of 16 bytes) into the cache at
     slots (int64 [tokens], page * page_size + row; negative: skipped; the others
-    distinct).  status: int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN.
+    distinct: tokens that share one leave a mixture of their bytes there).  status:
+    int32 [1] or None, NVFP4_ERR_NONFINITE after Inf or NaN.
     No gradient: K and V that require one are refused (but under torch.no_grad())."""
     d = _one_layer(cache)
     _kv_rows(K, "K", d.kv_heads, d.head_dim, cache._device, _TYPES)

@@ -633,8 +633,8 @@ enum nvfp4_type { NVFP4_TYPE_BF16 = 0, NVFP4_TYPE_FP16 = 1, NVFP4_TYPE_FP32 = 2 
  *              16-byte aligned, strides multiples of 16 bytes.
  *   slots      DEVICE int64 [tokens], 8-byte aligned.  A token whose slot is
  *              negative (padding) or not in the cache is skipped.  The other
- *              slots must be distinct: of tokens that share one, each group
- *              may come from any of them.
+ *              slots must be distinct: tokens that share one leave bytes of
+ *              each there, a group's codes of one and its scale of another.
  *   status     int, device scalar, may be NULL: the call first sets it to
  *              NVFP4_OK (an asynchronous memset); NVFP4_ERR_NONFINITE when a
  *              written group held Inf or NaN.
