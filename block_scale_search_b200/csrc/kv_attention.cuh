@@ -105,11 +105,10 @@ __device__ __forceinline__ float to_f32(uint16_t v, int type) {
 // top of FP16's range.  So rows of FP16 stay exact (shrink >= 1), and of a row
 // of BF16 all elements down to 2^-32 of the largest do; smaller ones are rounded
 // to steps of at most 2^-39 of it.  (Rows below 2^-111 lie lower in FP16: shrink
-// is at most 2^126, a finite number.)  A row that holds Inf goes all
-// to NaN: its scores could all be -inf, which stands for hidden ones.  `factor`
-// turns a dot product into a score in base 2.  It is kept above 0 (a negative
-// one turns the row's sign), so that it keeps the order of scores and a hidden
-// score's -inf.
+// is at most 2^126, a finite number.)  A row that holds Inf goes all to NaN: its
+// scores could all be -inf, which stands for hidden ones.  `factor` turns a dot
+// product into a score in base 2.  It is kept above 0 (a negative one turns the
+// row's sign), so that it keeps the order of scores and a hidden score's -inf.
 __device__ __forceinline__ void row_scale(float mx, float scale, float& shrink, float& factor) {
   const uint32_t e = min(max(__float_as_uint(mx) >> 23, 16u), 254u);
   shrink = __uint_as_float((269u - e) << 23);
