@@ -32,8 +32,8 @@
 // cycles of a scheduler each), against 745 cycles of a scheduler's share of
 // HBM; in the loop it takes about 870, that is 5.9 TB/s, also where the cache
 // lies in L2: what bounds it is instructions.  Over a whole call 4.3 TB/s (48
-// sequences of up to 8192 tokens, 64 / 8 heads of 128: 56.7 us) and 4.8 TB/s
-// (two of 131072: 62.7 us) remain: a CTA takes about 6 us until its first tile
+// sequences of up to 8192 tokens, 64 / 8 heads of 128: 57.0 us) and 4.8 TB/s
+// (two of 131072: 63.2 us) remain: a CTA takes about 6 us until its first tile
 // is there (lengths, page ids and tiles are three trips to memory one after
 // another) and 2 us to join its warps, the cut items 3 to 5 us.
 //

@@ -1,10 +1,13 @@
 // kv_cache.cu -- writing, reading and copying the paged NVFP4 K/V cache.
 //
-// All three are bound by HBM: append reads 2 (or 4) bytes an element and
-// writes 0.5625, read the reverse, copy moves bytes.  Measured with 8 heads of
-// 128: append of 16001 tokens 22 us (3.9 TB/s; 220 instructions a group of 16
-// keep the schedulers 60% busy beside it), read of 100003 tokens to FP16 88 us
-// (6.0 TB/s), copy of 511 pages in 16 layers 99 us (6.1 TB/s).
+// Append reads 2 (or 4) bytes an element and writes 0.5625, read the reverse,
+// copy moves bytes.  Measured with 8 heads of 128: append of 16001 tokens of 16
+// bits 21 us (4.0 TB/s; 220 instructions a group of 16 keep the schedulers 63%
+// busy beside it, neither is full: a warp's loads and its arithmetic take
+// turns) and of 32 bits 25 us (5.9 TB/s), read of 100003 tokens to FP16 88 us
+// (6.0 TB/s), copy of 511 pages in 16 layers 99 us (6.1 TB/s).  The last two are
+// bound by HBM.  A page and layer is copied by one CTA, for caches of small pages
+// and many layers: one page of 256 tokens in one layer takes 8 us, of 4096 101.
 #include <type_traits>
 
 #include <cuda_bf16.h>

@@ -19,10 +19,11 @@
 // threads hold a row's 128 scores at once.  A step takes 3400 cycles: a tile's
 // softmax 2400 (1900 of them in the exponentials, which both tiles share) and
 // then its MMAs 1024 before its next scores are there.  Measured: 4 chunks of
-// 2048 tokens over up to 8192, 32 / 8 heads of 128, 502 us or 1.04 PFLOP/s (63%
-// of the measured GEMM rate); 8000 tokens at once 1.06.  At head_dim 64 the
-// MMAs halve and the softmax does not: 8000 tokens at once 395 us for half the
-// work that takes 496 at 128.
+// 2048 tokens over up to 8192, 32 / 8 heads of 128, 508 us in short bursts or
+// 1.03 PFLOP/s (62% of the measured GEMM rate), 565 us back to back under the
+// power cap; 8000 tokens at once 1.06.  At head_dim 64 the MMAs halve and the
+// softmax does not: 8000 tokens at once 394 us for half the work that takes 498
+// at 128.
 // The cache is decoded once per CTA: 256 rows share it.  A decoded value (code
 // times scale) is exact in FP16; Q's rows are scaled by powers of two and P is
 // rounded as in kv_attention.cu, and the running maximum moves by the same
@@ -830,7 +831,12 @@ cudaError_t run_prompt(const Params& p, cudaStream_t stream) {
 // 256 rows by 128 tokens (1.7 us at head_dim 128): every wave of CTAs takes its
 // share of steps and about 4 more to start and finish; partial results cost
 // about 2 a wave's worth of them, and the joining kernel 3.  One sequence of 64
-// new tokens over 32000, 64 / 8 heads of 128, takes 428 us unsplit.
+// new tokens over 32000, 64 / 8 heads of 128, takes 75 us so and 428 unsplit.
+// The host knows bounds alone, so items are max_q rows of every sequence: those
+// that turn out empty still cost about half a microsecond of an SM each, and
+// count as items here (255 single tokens over 4000 beside a chunk of 2048, 32 / 8
+// heads, 1117 us, apart 223 and 114; 63 beside that one sequence 602, apart 68
+// and 75).
 PromptPlan prompt_plan(int64_t batch, int64_t rows, int64_t max_kv, int kv_heads, int num_sms) {
   PromptPlan best{};
   best.row_blocks = (rows + kRows - 1) / kRows;

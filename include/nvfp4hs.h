@@ -690,7 +690,10 @@ int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t cod
  *              out of range are clamped and never lead outside the buffers.
  *   max_q, max_kv  host bounds of Lq and Lk (longer ones are cut to them),
  *              0 <= max_kv <= table_stride * page_size; a captured call serves
- *              any lengths within them.
+ *              any lengths within them.  Where max_q tokens are more than 32 query
+ *              rows for a KV head (64 at head_dim 64), the call is laid out for
+ *              so many of every sequence: many single tokens beside one long
+ *              prompt take less time as two calls.
  *   causal     0 or 1; window >= 0, 0 for none; a window needs causal.
  *   batch      0 .. 65535; total_q, max_q < 2^31; q_heads a multiple of
  *              kv_heads, at most 1024.  Bounds whose work the kernels cannot
