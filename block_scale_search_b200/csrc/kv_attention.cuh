@@ -22,7 +22,9 @@ constexpr float kAim = 7.0f, kTop = 15.0f;
 // less.  Rows whose scores may lie further out (|q| is below 2^16, |k| at most
 // 6 * 448) have their exponents held at kTop: tokens with the largest score then
 // have equal weights and the others theirs, to what FP32 knows of such scores.
-// Holding takes an instruction a score, so the loops exist with and without.
+// Holding takes an instruction a score, so the loops exist with and without it
+// (a branch in one loop: the chunk case 520 us, so 508; 48 sequences of up to
+// 8192 tokens 57.1 and 57.0).
 __device__ __forceinline__ float m_for(float x, float f) { return __fadd_rd(__fmul_rd(x, f), -kAim); }
 template <int D>
 __device__ __forceinline__ bool may_pass_top(float f) { return !(f < 0x1p25f / (D * 65536.0f * 2688.0f)); }

@@ -703,11 +703,12 @@ int nvfp4_kv_copy_pages(const nvfp4_kv_cache* cache, int64_t layers, int64_t cod
  *   workspace  nvfp4_kv_attention_workspace_size() bytes (device dependent; 0
  *              for invalid arguments or no device), 256-byte aligned; needs no
  *              initialisation.  Calls that may overlap need one each.
- * FP32 sums and softmax statistics; for the tensor cores, probabilities are
- * rounded to FP16 (2^-11 of each down to 2^-21 of the row's largest, and 2^-32
- * of that largest below), and so are elements of a BF16 query that lie below
- * 2^-32 of their row's largest.  The result depends on the lengths, the bounds and the
- * number of SMs, not on timing. */
+ * FP32 sums and softmax statistics (where a sequence has many rows, a quarter of
+ * the exponentials are within 2.6e-6, the others within 2^-22).  For the tensor
+ * cores probabilities are rounded to FP16 (2^-11 of each down to 2^-21 of the
+ * row's largest, 2^-32 of that largest below), and so are elements of a BF16
+ * query that lie below 2^-32 of their row's largest.  The result depends on the
+ * lengths, the bounds and the number of SMs, not on timing. */
 size_t nvfp4_kv_attention_workspace_size(int64_t batch, int64_t max_q, int64_t max_kv, int q_heads,
                                          int kv_heads, int head_dim);
 int nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* Q, int type, int q_heads,
